@@ -2,7 +2,9 @@
 
 Thin Python binding over the C ABI in ``include/wkv.h`` and
 ``include/linattn.h`` (causal linear attention: ``linattn_forward``,
-``linattn_backward``).  The functions in
+``linattn_backward``; with a decay for each head: ``linattn_decay_forward``,
+``linattn_decay_backward``, ``linattn_decay_step``; rotary positions:
+``linattn_rotary``).  The functions in
 ``abi`` carry the C names and take raw device pointers (ints) -- argument
 marshalling only.  The tensor helpers below (``forward``, ``backward``,
 ``step``, ``WKV``, ``backward_state``, ``token_shift`` and the gated ``forward_gated``, ``backward_gated``,
@@ -16,7 +18,9 @@ There is no CPU or PyTorch fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import importlib
+import math
 
 from .constants import (WKV_BF16, WKV_F32, WKV_KERNEL_AUTO, WKV_KERNEL_CHUNKED,
                         WKV_KERNEL_CLUSTER, WKV_KERNEL_SEGMENT, WKV_KERNEL_TILE, WKV_KERNEL_CHAIN,
@@ -31,6 +35,9 @@ __all__ = [
     "forward_gated", "backward_gated", "WKV", "wkv", "WKVState", "wkv_state", "GatedWKV", "gated_wkv", "wkv_workspace_size", "wkv_ckpt_size", "wkv_strerror", "wkv_version",
     "library_path", "LINATTN_OP_FORWARD", "LINATTN_OP_BACKWARD", "linattn_workspace_size",
     "linattn_forward", "linattn_backward",
+    "linattn_decay_workspace_size", "linattn_decay_forward", "linattn_decay_backward", "linattn_decay_step",
+    "linattn_decay_status", "LinattnDecay", "linattn_decay", "linattn_decay_state",
+    "rotary_frequencies", "linattn_rotary", "Rotary", "rotary",
 ]
 
 
@@ -288,6 +295,361 @@ def linattn_backward(q, k, v, grad_out, *, out=None, grad_q=None, grad_k=None, g
         abi.check(abi.linattn_backward(BH, N, D, M, _ptr(q), _ptr(k), _ptr(v), _ptr(grad_out), _ptr(grad_q),
                                        _ptr(grad_k), _ptr(grad_v), _ptr(buf), nbytes, _stream(stream)))
     return grad_q, grad_k, grad_v
+
+
+# ------------------------- linear attention with a decay for each head ---
+
+def linattn_decay_workspace_size(op, B, T, H, D, M, dtype):
+    return _abi().linattn_decay_workspace_size(op, B, T, H, D, M, dtype)
+
+
+def _scope(t, stream):
+    """Context in which allocations and launches go to ``stream`` (default: the
+    current stream) of the tensor's device."""
+    torch = _torch()
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=t.device)
+        return torch.cuda.stream(stream)
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+_decay_status = {}
+
+
+def _status_ptr(device):
+    """The device's status word.  It is shared by every call (kernels only ever
+    store an error there) and lives as long as the process; a call captured
+    into a graph before any eager one goes without."""
+    torch = _torch()
+    t = _decay_status.get(device.index)
+    if t is None:
+        if torch.cuda.is_current_stream_capturing():
+            return 0
+        t = _decay_status[device.index] = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.current_stream(device).synchronize()  # zeroed before any other stream's call stores to it
+    return t.data_ptr()
+
+
+def linattn_decay_status(device=None):
+    """Device-side status of the ``linattn_decay_*`` calls made so far (0, or
+    WKV_ERR_TIMEOUT if a bounded wait gave up); waits for the device and clears it."""
+    torch = _torch()
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    t = _decay_status.get(device.index)
+    if t is None:
+        return 0
+    torch.cuda.synchronize(device)
+    rc = int(t.item())
+    if rc:
+        t.zero_()
+    return rc
+
+
+def _check_heads(ref, shape, dtype, **tensors):
+    """Each tensor is [.., D] of ``shape`` and ``dtype`` on ``ref``'s device with a contiguous feature index."""
+    for name, t in tensors.items():
+        if t.device != ref.device or not t.is_cuda:
+            raise ValueError(f"{name}: tensors must be on one CUDA device")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _check_plain(ref, **tensors):
+    """(tensor or None, shape, dtype): contiguous tensors on ``ref``'s device."""
+    for name, (t, shape, dtype) in tensors.items():
+        if t is None:
+            continue
+        if t.device != ref.device:
+            raise ValueError(f"{name}: tensors must be on one CUDA device")
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _view4(t):
+    s = t.stride()
+    return _abi().View(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _check_decay(q, k, v, log_decay, lengths, **states):
+    torch = _torch()
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k must be [B, T, H, D] and v [B, T, H, M]")
+    B, T, H, D = q.shape
+    M = v.shape[3]
+    _check_heads(q, q.shape, q.dtype, q=q, k=k)
+    _check_heads(q, (B, T, H, M), q.dtype, v=v)
+    _check_plain(q, log_decay=(log_decay, (H,), torch.float32), lengths=(lengths, (B,), torch.int32),
+                 **{n: (t, (B, H, D, M), torch.float32) for n, t in states.items()})
+    return B, T, H, D, M, _dtype_code(q)
+
+
+def _scratch(nbytes, device):
+    torch = _torch()
+    # per call, from torch's stream-ordered allocator: calls on other streams,
+    # in other threads or in captured graphs never share it
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def linattn_decay_forward(q, k, v, log_decay, state=None, *, scale=1.0, lengths=None, want_state=False, out=None,
+                          stream=None):
+    """Linear attention with a decay for each head (include/linattn.h):
+    out_t = scale * q_t^T S_t with S_t = e^{log_decay[h]} S_{t-1} + k_t v_t^T, for q, k [B, T, H, D] and
+    v [B, T, H, M] (float32 or bfloat16; any strides with a contiguous last dimension), log_decay [H]
+    float32 <= 0, the state before position 0 (``state`` [B, H, D, M] float32, or empty) and each row's
+    number of positions (``lengths`` [B] int32, or T for all; out is zero behind them).  Returns
+    (out [B, T, H, M], the state after each row's last position or None)."""
+    torch = _torch()
+    with _scope(q, stream):
+        B, T, H, D, M, dt = _check_decay(q, k, v, log_decay, lengths, state=state)
+        if out is None:
+            out = torch.empty((B, T, H, M), dtype=q.dtype, device=q.device)
+        else:
+            _check_heads(q, (B, T, H, M), q.dtype, out=out)
+        s_out = torch.empty((B, H, D, M), dtype=torch.float32, device=q.device) if want_state else None
+        abi = _abi()
+        need = abi.linattn_decay_workspace_size(LINATTN_OP_FORWARD, B, T, H, D, M, dt)
+        ws = _scratch(need, q.device)
+        abi.check(abi.linattn_decay_forward(B, T, H, D, M, dt, _view4(q), _view4(k), _view4(v), _ptr(log_decay),
+                                            scale, _ptr(lengths), _ptr(state), _view4(out), _ptr(s_out), _ptr(ws),
+                                            need, _status_ptr(q.device),
+                                            torch.cuda.current_stream(q.device).cuda_stream))
+    return out, s_out
+
+
+def linattn_decay_backward(q, k, v, log_decay, grad_out, state=None, *, scale=1.0, lengths=None, grad_state_out=None,
+                           want_grad_state=False, grad_q=None, grad_k=None, grad_v=None, stream=None):
+    """Gradients (grad_q, grad_k, grad_v, grad_state or None) of L for ``linattn_decay_forward`` with the same
+    arguments, given grad_out = dL/dout and, optionally, ``grad_state_out`` = dL/d(state after the last
+    position); grad_state is dL/dstate.  log_decay is a constant."""
+    torch = _torch()
+    with _scope(q, stream):
+        B, T, H, D, M, dt = _check_decay(q, k, v, log_decay, lengths, state=state, grad_state_out=grad_state_out)
+        _check_heads(q, (B, T, H, M), q.dtype, grad_out=grad_out)
+        new = lambda n: torch.empty((B, T, H, n), dtype=q.dtype, device=q.device)  # noqa: E731
+        grad_q = new(D) if grad_q is None else grad_q
+        grad_k = new(D) if grad_k is None else grad_k
+        grad_v = new(M) if grad_v is None else grad_v
+        _check_heads(q, (B, T, H, D), q.dtype, grad_q=grad_q, grad_k=grad_k)
+        _check_heads(q, (B, T, H, M), q.dtype, grad_v=grad_v)
+        gs = torch.empty((B, H, D, M), dtype=torch.float32, device=q.device) if want_grad_state else None
+        abi = _abi()
+        need = abi.linattn_decay_workspace_size(LINATTN_OP_BACKWARD, B, T, H, D, M, dt)
+        ws = _scratch(need, q.device)
+        abi.check(abi.linattn_decay_backward(B, T, H, D, M, dt, _view4(q), _view4(k), _view4(v), _ptr(log_decay),
+                                             scale, _ptr(lengths), _ptr(state), _view4(grad_out),
+                                             _ptr(grad_state_out), _view4(grad_q), _view4(grad_k), _view4(grad_v),
+                                             _ptr(gs), _ptr(ws), need, _status_ptr(q.device),
+                                             torch.cuda.current_stream(q.device).cuda_stream))
+    return grad_q, grad_k, grad_v, gs
+
+
+def linattn_decay_step(q, k, v, log_decay, state, *, scale=1.0, out=None, state_out=None, stream=None):
+    """One token for N sequences: q, k [N, H, D], v [N, H, M], state [N, H, D, M] float32.  ``state_out``
+    defaults to updating ``state`` in place.  Returns (out [N, H, M], state_out)."""
+    torch = _torch()
+    with _scope(q, stream):
+        if q.dim() != 3 or v.dim() != 3:
+            raise ValueError("q, k must be [N, H, D] and v [N, H, M]")
+        N, H, D = q.shape
+        M = v.shape[2]
+        _check_heads(q, q.shape, q.dtype, q=q, k=k)
+        _check_heads(q, (N, H, M), q.dtype, v=v)
+        if out is None:
+            out = torch.empty((N, H, M), dtype=q.dtype, device=q.device)
+        else:
+            _check_heads(q, (N, H, M), q.dtype, out=out)
+        if state_out is None:
+            state_out = state
+        f32 = torch.float32
+        _check_plain(q, log_decay=(log_decay, (H,), f32), state=(state, (N, H, D, M), f32),
+                     state_out=(state_out, (N, H, D, M), f32))
+        abi = _abi()
+        view = lambda t: abi.View(t.data_ptr(), t.stride(0), 0, t.stride(1))  # noqa: E731
+        abi.check(abi.linattn_decay_step(N, H, D, M, _dtype_code(q), view(q), view(k), view(v), _ptr(log_decay),
+                                         scale, _ptr(state), view(out), _ptr(state_out),
+                                         torch.cuda.current_stream(q.device).cuda_stream))
+    return out, state_out
+
+
+def _rows(t):
+    """A gradient or argument as the library takes it: expanded or transposed
+    ones are copied."""
+    if t is None or (t.stride(-1) == 1 and all(s > 0 or n <= 1 for s, n in zip(t.stride(), t.shape))):
+        return t
+    return t.contiguous()
+
+
+class LinattnDecay:
+    """torch.autograd.Function wrapper: (out, state_out) = LinattnDecay.apply(q, k, v, log_decay, state,
+    lengths, scale).  Gradients reach state through both out and state_out, so a sequence split across
+    calls back-propagates through the state (truncated BPTT)."""
+
+    _fn = None
+
+    @classmethod
+    def apply(cls, q, k, v, log_decay, state=None, lengths=None, scale=1.0, want_state=True):
+        if log_decay.requires_grad:
+            raise ValueError("log_decay is a constant of linattn_decay: it has no gradient (detach it)")
+        if cls._fn is None:
+            torch = _torch()
+            from torch.autograd.function import once_differentiable
+
+            class _F(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, q, k, v, log_decay, state, lengths, scale, want_state):
+                    ctx.set_materialize_grads(False)
+                    q, k, v = _rows(q), _rows(k), _rows(v)
+                    state = None if state is None else state.contiguous()
+                    out, s_out = linattn_decay_forward(q, k, v, log_decay, state, scale=scale, lengths=lengths,
+                                                       want_state=want_state)
+                    ctx.save_for_backward(q, k, v, log_decay, state, lengths)
+                    ctx.scale = scale
+                    return out, s_out
+
+                @staticmethod
+                @once_differentiable
+                def backward(ctx, go, gs):
+                    q, k, v, log_decay, state, lengths = ctx.saved_tensors
+                    go = torch.zeros_like(v) if go is None else go
+                    gq, gk, gv, gst = linattn_decay_backward(
+                        q, k, v, log_decay, _rows(go), state, scale=ctx.scale, lengths=lengths,
+                        grad_state_out=None if gs is None else gs.contiguous(),
+                        want_grad_state=state is not None and ctx.needs_input_grad[4])
+                    return gq, gk, gv, None, gst, None, None, None
+
+            cls._fn = _F
+        return cls._fn.apply(q, k, v, log_decay, state, lengths, scale, want_state)
+
+
+def linattn_decay(q, k, v, log_decay, state=None, *, lengths=None, scale=1.0):
+    """Differentiable ``linattn_decay_forward``: out [B, T, H, M]."""
+    return LinattnDecay.apply(q, k, v, log_decay, state, lengths, scale, False)[0]
+
+
+def linattn_decay_state(q, k, v, log_decay, state=None, *, lengths=None, scale=1.0):
+    """Differentiable ``linattn_decay_forward`` with the state: (out, state_out)."""
+    return LinattnDecay.apply(q, k, v, log_decay, state, lengths, scale, True)
+
+
+# ------------------------------------------------------- rotary positions ---
+
+def rotary_frequencies(rotated, *, base=10000.0, scaling="none", factor=1.0, trained_length=None, fast_turns=32.0,
+                       slow_turns=1.0, device=None):
+    """The plan of ``linattn_rotary``: (inv_freq [rotated / 2] float64, mscale) with inv_freq[i] =
+    base^(-2 i / rotated), stretched by ``factor`` for texts longer than those trained on:
+    "linear"    every frequency divided by factor (positions compressed);
+    "ntk"       base raised to base * factor^(rotated / (rotated - 2)): the slowest pair is stretched by
+                factor, the fastest not at all;
+    "by_parts"  pairs that turn more than ``fast_turns`` times over ``trained_length`` positions keep their
+                frequency, those under ``slow_turns`` are divided by factor, linear in between; mscale =
+                0.1 ln(factor) + 1."""
+    torch = _torch()
+    if rotated < 2 or rotated % 2:
+        raise ValueError("rotated must be even and at least 2")
+    if not (factor > 0 and base > 0):
+        raise ValueError("factor and base must be positive")
+    if scaling not in ("none", "linear", "ntk", "by_parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if scaling == "ntk" and rotated > 2:
+        base = base * factor ** (rotated / (rotated - 2))
+    f = float(base) ** (-torch.arange(0, rotated, 2, dtype=torch.float64) / rotated)
+    mscale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        if not trained_length or fast_turns <= slow_turns:
+            raise ValueError("by_parts needs trained_length and fast_turns > slow_turns")
+        keep = ((trained_length * f / (2 * math.pi) - slow_turns) / (fast_turns - slow_turns)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1 - keep)
+        mscale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    return f.to("cuda" if device is None else device), mscale
+
+
+def linattn_rotary(q, k, positions, inv_freq, *, mscale=1.0, interleaved=False, inverse=False, out_q=None, out_k=None,
+                   stream=None):
+    """Rotates the first 2 * len(inv_freq) elements of every head of q [B, T, Hq, D] and k [B, T, Hk, D] (or
+    None) by ``positions`` ([B, T] or [T], int32 or int64) times ``inv_freq`` (float64, from
+    ``rotary_frequencies``); pairs are (i, i + R/2), or (2i, 2i + 1) if ``interleaved``.  ``inverse``
+    rotates back.  ``out_q`` / ``out_k`` may be q / k (in place).  Returns (out_q, out_k)."""
+    torch = _torch()
+    with _scope(q, stream):
+        if q.dim() != 4 or (k is not None and k.dim() != 4):
+            raise ValueError("q and k must be [B, T, heads, D]")
+        B, T, Hq, D = q.shape
+        Hk = 0 if k is None else k.shape[2]
+        if positions.dtype not in (torch.int32, torch.int64) or tuple(positions.shape) not in ((T,), (B, T)):
+            raise ValueError("positions must be int32 or int64, [T] or [B, T]")
+        if positions.device != q.device or (T > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions must be on q's device, contiguous along T")
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a float64 vector")
+        R = 2 * inv_freq.shape[0]
+        _check_plain(q, inv_freq=(inv_freq, inv_freq.shape, torch.float64))
+        _check_heads(q, q.shape, q.dtype, q=q)
+        if out_q is None:
+            out_q = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device)
+        else:
+            _check_heads(q, q.shape, q.dtype, out_q=out_q)
+        if k is not None:
+            _check_heads(q, (B, T, Hk, D), q.dtype, k=k)
+            if out_k is None:
+                out_k = torch.empty((B, T, Hk, D), dtype=q.dtype, device=q.device)
+            else:
+                _check_heads(q, k.shape, q.dtype, out_k=out_k)
+        elif out_k is not None:
+            raise ValueError("out_k without k")
+        abi = _abi()
+        abi.check(abi.linattn_rotary(B, T, D, R, _dtype_code(q), Hq, _view4(q), Hk,
+                                     None if k is None else _view4(k), positions.data_ptr(),
+                                     positions.element_size(), positions.stride(0) if positions.dim() == 2 else 0,
+                                     inv_freq.data_ptr(), mscale, int(interleaved), int(inverse), _view4(out_q),
+                                     None if k is None else _view4(out_k),
+                                     torch.cuda.current_stream(q.device).cuda_stream))
+    return out_q, out_k
+
+
+class Rotary:
+    """torch.autograd.Function wrapper: (q', k') = Rotary.apply(q, k, positions, inv_freq, mscale, interleaved);
+    the gradient is the inverse rotation."""
+
+    _fn = None
+
+    @classmethod
+    def apply(cls, q, k, positions, inv_freq, mscale=1.0, interleaved=False):
+        if cls._fn is None:
+            torch = _torch()
+            from torch.autograd.function import once_differentiable
+
+            class _F(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, q, k, positions, inv_freq, mscale, interleaved):
+                    ctx.save_for_backward(positions, inv_freq)
+                    ctx.how = dict(mscale=mscale, interleaved=interleaved)
+                    return linattn_rotary(_rows(q), _rows(k), positions, inv_freq, **ctx.how)
+
+                @staticmethod
+                @once_differentiable
+                def backward(ctx, gq, gk):
+                    positions, inv_freq = ctx.saved_tensors
+                    gq, gk = linattn_rotary(_rows(gq), _rows(gk), positions, inv_freq, inverse=True, **ctx.how)
+                    return gq, gk, None, None, None, None
+
+            cls._fn = _F
+        return cls._fn.apply(q, k, positions, inv_freq, mscale, interleaved)
+
+
+def rotary(q, k, positions, inv_freq, *, mscale=1.0, interleaved=False):
+    """Differentiable ``linattn_rotary``: (q', k')."""
+    return Rotary.apply(q, k, positions, inv_freq, mscale, interleaved)
 
 
 def token_shift(x, mu, x_prev=None, *, out=None, stream=None):

@@ -27,6 +27,8 @@ EXPORTS = (
     "wkv_strerror", "wkv_last_cuda_error", "wkv_cuda_error_name", "wkv_version",
     # include/linattn.h
     "linattn_workspace_size", "linattn_forward", "linattn_backward", "linattn_backward_saved",
+    "linattn_decay_workspace_size", "linattn_decay_forward", "linattn_decay_backward", "linattn_decay_step",
+    "linattn_rotary",
 )
 
 
@@ -34,6 +36,12 @@ class Options(ctypes.Structure):
     """wkv_options: kernel selector, test hook, look-back wait limit."""
     _fields_ = [("kernel", ctypes.c_int), ("test_hold_first_chunk", ctypes.c_int),
                 ("spin_limit", ctypes.c_int64)]
+
+
+class View(ctypes.Structure):
+    """linattn_view: a device pointer and the strides (in elements) of batch, time and head."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
 
 
 if not os.path.exists(LIB_PATH):
@@ -44,6 +52,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 _i64, _int, _sz, _p = ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
 _opt = ctypes.POINTER(Options)
+_view, _f32 = ctypes.POINTER(View), ctypes.c_float
 
 _SIGS = {
     "wkv_workspace_size": (_sz, [_int, _i64, _i64, _i64, _int]),
@@ -78,6 +87,14 @@ _SIGS = {
     "linattn_forward": (_int, [_i64, _i64, _int, _int, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "linattn_backward": (_int, [_i64, _i64, _int, _int] + [_p] * 7 + [_p, _sz, _p]),
     "linattn_backward_saved": (_int, [_i64, _i64, _int, _int] + [_p] * 8 + [_p, _sz, _p]),
+    "linattn_decay_workspace_size": (_sz, [_int, _i64, _i64, _i64, _int, _int, _int]),
+    "linattn_decay_forward": (_int, [_i64] * 3 + [_int] * 3 + [_view] * 3 + [_p, _f32, _p, _p, _view, _p, _p, _sz, _p,
+                                                                         _p]),
+    "linattn_decay_backward": (_int, [_i64] * 3 + [_int] * 3 + [_view] * 3 + [_p, _f32, _p, _p, _view, _p] +
+                               [_view] * 3 + [_p, _p, _sz, _p, _p]),
+    "linattn_decay_step": (_int, [_i64] * 2 + [_int] * 3 + [_view] * 3 + [_p, _f32, _p, _view, _p, _p]),
+    "linattn_rotary": (_int, [_i64, _i64, _int, _int, _int, _i64, _view, _i64, _view, _p, _int, _i64, _p, _f32, _int,
+                              _int, _view, _view, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -239,6 +256,38 @@ def linattn_backward(BH, N, D, M, q, k, v, grad_out, grad_q, grad_k, grad_v, ws,
 def linattn_backward_saved(BH, N, D, M, q, k, v, out, grad_out, grad_q, grad_k, grad_v, ws, ws_bytes, stream):
     return lib.linattn_backward_saved(BH, N, D, M, q, k, v, out, grad_out, grad_q, grad_k, grad_v, ws, ws_bytes,
                                       stream)
+
+
+def _v(view):
+    return None if view is None else ctypes.byref(view)
+
+
+def linattn_decay_workspace_size(op, B, T, H, D, M, dtype):
+    return lib.linattn_decay_workspace_size(op, B, T, H, D, M, dtype)
+
+
+def linattn_decay_forward(B, T, H, D, M, dtype, q, k, v, log_decay, scale, lengths, state_in, out, state_out, ws,
+                          ws_bytes, status, stream):
+    return lib.linattn_decay_forward(B, T, H, D, M, dtype, _v(q), _v(k), _v(v), log_decay, scale, lengths, state_in,
+                                     _v(out), state_out, ws, ws_bytes, status, stream)
+
+
+def linattn_decay_backward(B, T, H, D, M, dtype, q, k, v, log_decay, scale, lengths, state_in, grad_out,
+                           grad_state_out, grad_q, grad_k, grad_v, grad_state_in, ws, ws_bytes, status, stream):
+    return lib.linattn_decay_backward(B, T, H, D, M, dtype, _v(q), _v(k), _v(v), log_decay, scale, lengths, state_in,
+                                      _v(grad_out), grad_state_out, _v(grad_q), _v(grad_k), _v(grad_v),
+                                      grad_state_in, ws, ws_bytes, status, stream)
+
+
+def linattn_decay_step(N, H, D, M, dtype, q, k, v, log_decay, scale, state_in, out, state_out, stream):
+    return lib.linattn_decay_step(N, H, D, M, dtype, _v(q), _v(k), _v(v), log_decay, scale, state_in, _v(out),
+                                  state_out, stream)
+
+
+def linattn_rotary(B, T, D, R, dtype, Hq, q, Hk, k, positions, pos_bytes, pos_stride_b, inv_freq, mscale, interleaved,
+                   inverse, out_q, out_k, stream):
+    return lib.linattn_rotary(B, T, D, R, dtype, Hq, _v(q), Hk, _v(k), positions, pos_bytes, pos_stride_b, inv_freq,
+                              mscale, interleaved, inverse, _v(out_q), _v(out_k), stream)
 
 
 def check(rc: int) -> None:

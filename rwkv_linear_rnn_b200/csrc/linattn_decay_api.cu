@@ -1,0 +1,234 @@
+// linattn_decay_api.cu -- host side of linear attention with a decay for each
+// head: argument checks, the choice of kernel and of segments, launches
+// (C ABI in include/linattn.h).
+#include <algorithm>
+#include <utility>
+
+#include "../../include/linattn.h"
+#include "../../include/wkv.h"
+#include "linattn_decay.cuh"
+
+namespace {
+using namespace wkv;
+using namespace wkv::decay;
+
+int rc_of(cudaError_t e) { return e == cudaSuccess ? WKV_OK : WKV_ERR_CUDA; }
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+size_t elem(int dtype) { return dtype == WKV_F32 ? 4 : 2; }
+
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 148;
+  return n;
+}
+
+struct Dims {
+  int64_t B, T, H;
+  int D, M, dtype;
+};
+int check_dims(const Dims &d) {
+  if (d.B < 1 || d.H < 1 || d.T < 0 || d.T >= (int64_t(1) << 31) || d.B >= (int64_t(1) << 24) ||
+      d.H >= (int64_t(1) << 24) || d.B * d.H >= (int64_t(1) << 24) || d.D < 1 || d.M < 1)
+    return WKV_ERR_INVALID_ARG;
+  if (d.dtype != WKV_F32 && d.dtype != WKV_BF16) return WKV_ERR_INVALID_ARG;
+  return d.D > kMaxHead || d.M > kMaxHead ? WKV_ERR_UNSUPPORTED : WKV_OK;
+}
+
+// A view's pointer and strides; an output's positions must not overlap each
+// other: sorted by stride, each dimension steps over the one below it.
+int check_view(const linattn_view *v, int64_t n0, int64_t n1, int64_t n2, int width, int dtype, bool output) {
+  if (!v || !v->ptr || v->stride_b < 0 || v->stride_t < 0 || v->stride_h < 0) return WKV_ERR_INVALID_ARG;
+  if (!aligned(v->ptr, elem(dtype))) return WKV_ERR_UNSUPPORTED;
+  constexpr int64_t kMost = int64_t(1) << 40;
+  if ((n0 > 1 && v->stride_b > kMost) || (n1 > 1 && v->stride_t > kMost) || (n2 > 1 && v->stride_h > kMost))
+    return WKV_ERR_INVALID_ARG;
+  if (output) {
+    std::pair<int64_t, int64_t> d[3] = {{v->stride_b, n0}, {v->stride_t, n1}, {v->stride_h, n2}};
+    std::sort(d, d + 3);
+    int64_t span = width;
+    for (const auto &x : d) {
+      if (x.second <= 1) continue;
+      if (x.first < span) return WKV_ERR_INVALID_ARG;
+      span += x.first * (x.second - 1);
+    }
+  }
+  return WKV_OK;
+}
+// First failure among several checks.
+int first_of(std::initializer_list<int> rcs) {
+  for (int rc : rcs)
+    if (rc != WKV_OK) return rc;
+  return WKV_OK;
+}
+bool overlap(const void *a, const void *b, size_t bytes) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + bytes && y < x + bytes;
+}
+
+View view(const linattn_view *v) { return View{v->ptr, v->stride_b, v->stride_t, v->stride_h}; }
+
+// Segments per head of the recurrence kernel.  One head's segment is a chain
+// of dependent positions run by Y / 16 warps; below about two warps per
+// scheduler the chain's latency shows, so heads are split until there are
+// that many, down to 64 positions per segment (the sums' pass and the scan
+// cost about 2/3 of an output pass, and each segment one state of traffic).
+int64_t rec_segments(int64_t BH, int64_t T, int Y, int sms) {
+  const int64_t warps = BH * ((Y + 15) / 16), want = 8 * (int64_t)sms;
+  if (warps * 2 >= want) return 1;
+  return std::max<int64_t>(1, std::min((want + warps - 1) / warps, T / 64));
+}
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+size_t seg_bytes(const Dims &d, int64_t nseg) { return nseg > 1 ? up256(sizeof(float) * d.B * d.H * nseg * d.D * d.M) : 0; }
+
+// Bytes that the passes of one call need: they run one after the other and
+// share one buffer.
+size_t pass_bytes(const Dims &d, int X, int Y) {
+  (void)X;
+  return seg_bytes(d, rec_segments(d.B * d.H, d.T, Y, num_sms()));
+}
+size_t workspace(int op, const Dims &d) {
+  const size_t f = pass_bytes(d, d.D, d.M);
+  return op == LINATTN_OP_FORWARD ? f : std::max(f, pass_bytes(d, d.M, d.D));
+}
+int check_ws(size_t need, const void *ws, size_t bytes) {
+  if (need == 0) return WKV_OK;
+  return !ws || !aligned(ws, 256) || bytes < need ? WKV_ERR_WORKSPACE : WKV_OK;
+}
+
+// One pass: segment sums and their scan if the heads are split, then the
+// outputs.
+cudaError_t run_pass(Pass p, const Dims &d, void *ws, cudaStream_t st) {
+  p.seg = static_cast<float *>(ws);
+  p.nseg = (int)rec_segments(d.B * d.H, d.T, p.Y, num_sms());
+  p.seg_len = (p.T + p.nseg - 1) / p.nseg;
+  cudaError_t e = cudaSuccess;
+  if (p.nseg > 1) {
+    e = launch_rec(p, d.dtype, true, st);
+    if (e == cudaSuccess) e = launch_scan(p, st);
+  }
+  return e == cudaSuccess ? launch_rec(p, d.dtype, false, st) : e;
+}
+
+// T = 0, or no work at all: the state goes through.
+int pass_state_through(const Dims &d, const float *in, float *out, cudaStream_t st) {
+  if (!out || in == out) return WKV_OK;
+  const size_t bytes = sizeof(float) * d.B * d.H * d.D * d.M;
+  return rc_of(in ? cudaMemcpyAsync(out, in, bytes, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(out, 0, bytes, st));
+}
+}  // namespace
+
+extern "C" size_t linattn_decay_workspace_size(int op, int64_t B, int64_t T, int64_t H, int D, int M, int dtype) {
+  const Dims d{B, T, H, D, M, dtype};
+  if ((op != LINATTN_OP_FORWARD && op != LINATTN_OP_BACKWARD) || check_dims(d) != WKV_OK) return 0;
+  return workspace(op, d);
+}
+
+extern "C" int linattn_decay_forward(int64_t B, int64_t T, int64_t H, int D, int M, int dtype, const linattn_view *q,
+                                     const linattn_view *k, const linattn_view *v, const float *log_decay, float scale,
+                                     const int32_t *lengths, const float *state_in, const linattn_view *out,
+                                     float *state_out, void *ws, size_t ws_bytes, int32_t *status, void *stream) {
+  const Dims d{B, T, H, D, M, dtype};
+  int rc = check_dims(d);
+  if (rc != WKV_OK) return rc;
+  if (!log_decay) return WKV_ERR_INVALID_ARG;
+  if (T > 0) {  // empty tensors may be null
+    rc = first_of({check_view(q, B, T, H, D, dtype, false), check_view(k, B, T, H, D, dtype, false),
+                   check_view(v, B, T, H, M, dtype, false), check_view(out, B, T, H, M, dtype, true)});
+    if (rc != WKV_OK) return rc;
+    if (out->ptr == q->ptr || out->ptr == k->ptr || out->ptr == v->ptr) return WKV_ERR_INVALID_ARG;
+  }
+  if (!aligned(log_decay, 4) || !aligned(lengths, 4) || !aligned(status, 4) || !aligned(state_in, 16) ||
+      !aligned(state_out, 16))
+    return WKV_ERR_UNSUPPORTED;
+  if (state_in != state_out && overlap(state_in, state_out, sizeof(float) * B * H * D * M)) return WKV_ERR_UNSUPPORTED;
+  rc = check_ws(workspace(LINATTN_OP_FORWARD, d), ws, ws_bytes);
+  if (rc != WKV_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) return pass_state_through(d, state_in, state_out, st);
+  Pass p{};
+  p.B = B, p.T = T, p.H = H, p.X = D, p.Y = M;
+  p.a = view(q), p.b = view(k), p.c = view(v), p.o = view(out);
+  p.log_decay = log_decay, p.lengths = lengths, p.s_in = state_in, p.s_out = state_out;
+  p.si = scale, p.sk = 1.f, p.status = status;
+  return rc_of(run_pass(p, d, ws, st));
+}
+
+extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, int M, int dtype, const linattn_view *q,
+                                      const linattn_view *k, const linattn_view *v, const float *log_decay,
+                                      float scale, const int32_t *lengths, const float *state_in,
+                                      const linattn_view *grad_out, const float *grad_state_out,
+                                      const linattn_view *grad_q, const linattn_view *grad_k,
+                                      const linattn_view *grad_v, float *grad_state_in, void *ws, size_t ws_bytes,
+                                      int32_t *status, void *stream) {
+  const Dims d{B, T, H, D, M, dtype};
+  int rc = check_dims(d);
+  if (rc != WKV_OK) return rc;
+  if (!log_decay) return WKV_ERR_INVALID_ARG;
+  if (T > 0) {
+    rc = first_of({check_view(q, B, T, H, D, dtype, false), check_view(k, B, T, H, D, dtype, false),
+                   check_view(v, B, T, H, M, dtype, false), check_view(grad_out, B, T, H, M, dtype, false),
+                   check_view(grad_q, B, T, H, D, dtype, true), check_view(grad_k, B, T, H, D, dtype, true),
+                   check_view(grad_v, B, T, H, M, dtype, true)});
+    if (rc != WKV_OK) return rc;
+    const void *outs[3] = {grad_q->ptr, grad_k->ptr, grad_v->ptr};
+    for (int i = 0; i < 3; ++i) {
+      for (const linattn_view *in : {q, k, v, grad_out})
+        if (outs[i] == in->ptr) return WKV_ERR_INVALID_ARG;
+      if (outs[i] == outs[(i + 1) % 3]) return WKV_ERR_INVALID_ARG;
+    }
+  }
+  if (!aligned(log_decay, 4) || !aligned(lengths, 4) || !aligned(status, 4) || !aligned(state_in, 16) ||
+      !aligned(grad_state_out, 16) || !aligned(grad_state_in, 16))
+    return WKV_ERR_UNSUPPORTED;
+  const size_t sbytes = sizeof(float) * B * H * D * M;
+  if (overlap(grad_state_in, state_in, sbytes) || overlap(grad_state_in, grad_state_out, sbytes))
+    return WKV_ERR_UNSUPPORTED;
+  rc = check_ws(workspace(LINATTN_OP_BACKWARD, d), ws, ws_bytes);
+  if (rc != WKV_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) return pass_state_through(d, grad_state_out, grad_state_in, st);
+  Pass p{};
+  p.B = B, p.T = T, p.H = H;
+  p.log_decay = log_decay, p.lengths = lengths, p.status = status;
+  // grad_q: forward in time, the state transposed
+  p.X = M, p.Y = D;
+  p.a = view(grad_out), p.b = view(v), p.c = view(k), p.o = view(grad_q);
+  p.s_in = state_in, p.s_in_t = 1;
+  p.si = scale, p.sk = 1.f;
+  cudaError_t e = run_pass(p, d, ws, st);
+  // grad_k: reverse, the state's adjoint transposed
+  p.a = view(v), p.b = view(grad_out), p.c = view(q), p.o = view(grad_k);
+  p.s_in = grad_state_out;
+  p.si = 1.f, p.sk = scale, p.reverse = 1;
+  if (e == cudaSuccess) e = run_pass(p, d, ws, st);
+  // grad_v and the gradient of the state handed in
+  p.X = D, p.Y = M;
+  p.a = view(k), p.b = view(q), p.c = view(grad_out), p.o = view(grad_v);
+  p.s_in_t = 0, p.s_out = grad_state_in;
+  if (e == cudaSuccess) e = run_pass(p, d, ws, st);
+  return rc_of(e);
+}
+
+extern "C" int linattn_decay_step(int64_t N, int64_t H, int D, int M, int dtype, const linattn_view *q,
+                                  const linattn_view *k, const linattn_view *v, const float *log_decay, float scale,
+                                  const float *state_in, const linattn_view *out, float *state_out, void *stream) {
+  if (N < 1 || H < 1 || N >= (int64_t(1) << 31) || H >= (int64_t(1) << 31) || N * H >= (int64_t(1) << 31) || D < 1 ||
+      M < 1 || (dtype != WKV_F32 && dtype != WKV_BF16) || !log_decay || !state_in || !state_out)
+    return WKV_ERR_INVALID_ARG;
+  if (D > kMaxHead || M > kMaxHead) return WKV_ERR_UNSUPPORTED;
+  linattn_view w[4];
+  const linattn_view *in[4] = {q, k, v, out};
+  for (int i = 0; i < 4; ++i) {
+    if (!in[i]) return WKV_ERR_INVALID_ARG;
+    w[i] = *in[i];
+    w[i].stride_t = 0;  // one position
+    const int rc = check_view(&w[i], N, 1, H, i < 2 ? D : M, dtype, i == 3);
+    if (rc != WKV_OK) return rc;
+  }
+  if (out->ptr == q->ptr || out->ptr == k->ptr || out->ptr == v->ptr) return WKV_ERR_INVALID_ARG;
+  if (!aligned(log_decay, 4) || !aligned(state_in, 16) || !aligned(state_out, 16)) return WKV_ERR_UNSUPPORTED;
+  if (state_in != state_out && overlap(state_in, state_out, sizeof(float) * N * H * D * M)) return WKV_ERR_UNSUPPORTED;
+  const decay::StepArgs s{N, H, D, M, view(&w[0]), view(&w[1]), view(&w[2]), view(&w[3]), log_decay, scale, state_in, state_out};
+  return rc_of(launch_step(s, dtype, static_cast<cudaStream_t>(stream)));
+}
