@@ -48,6 +48,7 @@ struct Pass {
   const float *s_in;       // [B, H, X, Y], or [B, H, Y, X] if s_in_t; or null
   int s_in_t;
   float *s_out;            // [B, H, X, Y] or null
+  int exact_state;         // the pass is one whose state a call may ask for: it is kept to 24 bits
   float si, sk;            // factors of the output and of the products entering the state
   int reverse;
   int nseg;                // segments per head
@@ -81,6 +82,12 @@ __device__ __forceinline__ float decayed(float x, Decay d) { return fmaf(x, d.m,
 // Launches.  Each returns the first launch's failure.
 cudaError_t launch_rec(const Pass &p, int dtype, bool sums_only, cudaStream_t st);
 cudaError_t launch_scan(const Pass &p, cudaStream_t st);
+// The tensor-core pass (bfloat16): whether it can take the views, its segments
+// per head and their length, and its launches.
+bool tc_fits(const Pass &p);
+int64_t tc_segments(int64_t BH, int64_t T, int sms);
+int64_t tc_segment_len(int64_t T, int64_t nseg);
+cudaError_t launch_tc(const Pass &p, bool sums_only, cudaStream_t st);
 struct StepArgs {
   int64_t N, H;
   int D, M;

@@ -81,15 +81,20 @@ int64_t rec_segments(int64_t BH, int64_t T, int Y, int sms) {
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t seg_bytes(const Dims &d, int64_t nseg) { return nseg > 1 ? up256(sizeof(float) * d.B * d.H * nseg * d.D * d.M) : 0; }
 
+// Whether a call's passes run on the tensor cores, as far as its sizes say.
+// Up to 32 positions a chunk of 128 is mostly padding.
+bool uses_tc(const Dims &d) { return d.dtype == WKV_BF16 && d.T > 32 && d.D % 8 == 0 && d.M % 8 == 0; }
+
 // Bytes that the passes of one call need: they run one after the other and
 // share one buffer.
-size_t pass_bytes(const Dims &d, int X, int Y) {
-  (void)X;
-  return seg_bytes(d, rec_segments(d.B * d.H, d.T, Y, num_sms()));
+size_t pass_bytes(const Dims &d, int Y) {
+  const int64_t BH = d.B * d.H;
+  const size_t rec = seg_bytes(d, rec_segments(BH, d.T, Y, num_sms()));
+  return uses_tc(d) ? std::max(rec, seg_bytes(d, tc_segments(BH, d.T, num_sms()))) : rec;
 }
 size_t workspace(int op, const Dims &d) {
-  const size_t f = pass_bytes(d, d.D, d.M);
-  return op == LINATTN_OP_FORWARD ? f : std::max(f, pass_bytes(d, d.M, d.D));
+  const size_t f = pass_bytes(d, d.M);
+  return op == LINATTN_OP_FORWARD ? f : std::max(f, pass_bytes(d, d.D));
 }
 int check_ws(size_t need, const void *ws, size_t bytes) {
   if (need == 0) return WKV_OK;
@@ -100,14 +105,21 @@ int check_ws(size_t need, const void *ws, size_t bytes) {
 // outputs.
 cudaError_t run_pass(Pass p, const Dims &d, void *ws, cudaStream_t st) {
   p.seg = static_cast<float *>(ws);
-  p.nseg = (int)rec_segments(d.B * d.H, d.T, p.Y, num_sms());
-  p.seg_len = (p.T + p.nseg - 1) / p.nseg;
+  const bool tc = uses_tc(d) && tc_fits(p);
+  if (tc) {
+    p.nseg = (int)tc_segments(d.B * d.H, d.T, num_sms());
+    p.seg_len = tc_segment_len(d.T, p.nseg);
+  } else {
+    p.nseg = (int)rec_segments(d.B * d.H, d.T, p.Y, num_sms());
+    p.seg_len = (p.T + p.nseg - 1) / p.nseg;
+  }
+  auto launch = [&](bool sums_only) { return tc ? launch_tc(p, sums_only, st) : launch_rec(p, d.dtype, sums_only, st); };
   cudaError_t e = cudaSuccess;
   if (p.nseg > 1) {
-    e = launch_rec(p, d.dtype, true, st);
+    e = launch(true);
     if (e == cudaSuccess) e = launch_scan(p, st);
   }
-  return e == cudaSuccess ? launch_rec(p, d.dtype, false, st) : e;
+  return e == cudaSuccess ? launch(false) : e;
 }
 
 // T = 0, or no work at all: the state goes through.
@@ -149,7 +161,7 @@ extern "C" int linattn_decay_forward(int64_t B, int64_t T, int64_t H, int D, int
   Pass p{};
   p.B = B, p.T = T, p.H = H, p.X = D, p.Y = M;
   p.a = view(q), p.b = view(k), p.c = view(v), p.o = view(out);
-  p.log_decay = log_decay, p.lengths = lengths, p.s_in = state_in, p.s_out = state_out;
+  p.log_decay = log_decay, p.lengths = lengths, p.s_in = state_in, p.s_out = state_out, p.exact_state = 1;
   p.si = scale, p.sk = 1.f, p.status = status;
   return rc_of(run_pass(p, d, ws, st));
 }
@@ -205,7 +217,7 @@ extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, in
   // grad_v and the gradient of the state handed in
   p.X = D, p.Y = M;
   p.a = view(k), p.b = view(q), p.c = view(grad_out), p.o = view(grad_v);
-  p.s_in_t = 0, p.s_out = grad_state_in;
+  p.s_in_t = 0, p.s_out = grad_state_in, p.exact_state = 1;
   if (e == cudaSuccess) e = run_pass(p, d, ws, st);
   return rc_of(e);
 }
