@@ -18,7 +18,8 @@ There is no CPU or PyTorch fallback.
 """
 from __future__ import annotations
 
-import contextlib
+import array
+import functools
 import importlib
 import math
 
@@ -50,6 +51,7 @@ def __getattr__(name):
     raise AttributeError(name)
 
 
+@functools.lru_cache(maxsize=None)
 def _abi():
     return importlib.import_module(".abi", __name__)
 
@@ -311,26 +313,25 @@ def _scope(t, stream):
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=t.device)
         return torch.cuda.stream(stream)
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
     return torch.cuda.device(t.device)
 
 
-_decay_status = {}
+_decay_status = {}  # device index -> (the device's status word, its address)
 
 
-def _status_ptr(device):
-    """The device's status word.  It is shared by every call (kernels only ever
+def _status_ptr(ref, dev):
+    """The status word of ``ref``'s device.  It is shared by every call (kernels only ever
     store an error there) and lives as long as the process; a call captured
     into a graph before any eager one goes without."""
-    torch = _torch()
-    t = _decay_status.get(device.index)
-    if t is None:
+    known = _decay_status.get(dev)
+    if known is None:
+        torch = _torch()
         if torch.cuda.is_current_stream_capturing():
             return 0
-        t = _decay_status[device.index] = torch.zeros(1, dtype=torch.int32, device=device)
-        torch.cuda.current_stream(device).synchronize()  # zeroed before any other stream's call stores to it
-    return t.data_ptr()
+        t = ref.new_zeros(1, dtype=torch.int32)
+        torch.cuda.current_stream(dev).synchronize()  # zeroed before any other stream's call stores to it
+        known = _decay_status[dev] = (t, t.data_ptr())
+    return known[1]
 
 
 def linattn_decay_status(device=None):
@@ -338,9 +339,10 @@ def linattn_decay_status(device=None):
     WKV_ERR_TIMEOUT if a bounded wait gave up); waits for the device and clears it."""
     torch = _torch()
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    t = _decay_status.get(device.index)
-    if t is None:
+    known = _decay_status.get(device.index)
+    if known is None:
         return 0
+    t = known[0]
     torch.cuda.synchronize(device)
     rc = int(t.item())
     if rc:
@@ -348,55 +350,61 @@ def linattn_decay_status(device=None):
     return rc
 
 
-def _check_heads(ref, shape, dtype, **tensors):
-    """Each tensor is [.., D] of ``shape`` and ``dtype`` on ``ref``'s device with a contiguous feature index."""
-    for name, t in tensors.items():
-        if t.device != ref.device or not t.is_cuda:
-            raise ValueError(f"{name}: tensors must be on one CUDA device")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError(f"{name}: the last dimension must be contiguous")
+# The checks below are most of a short call's time: they compare each property
+# once and gather the views on the way.
 
-
-def _check_plain(ref, **tensors):
-    """(tensor or None, shape, dtype): contiguous tensors on ``ref``'s device."""
-    for name, (t, shape, dtype) in tensors.items():
-        if t is None:
-            continue
-        if t.device != ref.device:
-            raise ValueError(f"{name}: tensors must be on one CUDA device")
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-
-
-def _view4(t):
+def _head_view(words, name, t, dev, dtype, shape):
+    """Appends the linattn_view of ``t``, which is of ``shape`` (4 or, for single tokens, 3 dimensions) and
+    ``dtype`` on device ``dev`` with a contiguous last dimension."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensors must be on one CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     s = t.stride()
-    return _abi().View(t.data_ptr(), s[0], s[1], s[2])
+    if s[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    words += (t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else (t.data_ptr(), s[0], 0, s[1])
 
 
-def _check_decay(q, k, v, log_decay, lengths, **states):
-    torch = _torch()
-    if q.dim() != 4 or v.dim() != 4:
-        raise ValueError("q, k must be [B, T, H, D] and v [B, T, H, M]")
-    B, T, H, D = q.shape
-    M = v.shape[3]
-    _check_heads(q, q.shape, q.dtype, q=q, k=k)
-    _check_heads(q, (B, T, H, M), q.dtype, v=v)
-    _check_plain(q, log_decay=(log_decay, (H,), torch.float32), lengths=(lengths, (B,), torch.int32),
-                 **{n: (t, (B, H, D, M), torch.float32) for n, t in states.items()})
-    return B, T, H, D, M, _dtype_code(q)
+def _plain_ptr(name, t, dev, dtype, shape):
+    """Address of a contiguous tensor of ``shape`` and ``dtype`` on device ``dev``; 0 for None."""
+    if t is None:
+        return 0
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensors must be on one CUDA device")
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _scratch(nbytes, device):
-    torch = _torch()
+def _on_device(q):
+    """q's device index, which must be a CUDA device's, and whether it is the current one."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on one CUDA device")
+    return dev, dev == _torch().cuda.current_device()
+
+
+@functools.lru_cache(maxsize=1024)
+def _decay_need(dev, op, B, T, H, D, M, dt):
+    # it depends on the current device's size too: callers have made dev current
+    return _abi().linattn_decay_workspace_size(op, B, T, H, D, M, dt)
+
+
+def _scratch(ref, nbytes):
     # per call, from torch's stream-ordered allocator: calls on other streams,
     # in other threads or in captured graphs never share it
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    return ref.new_empty(nbytes, dtype=_torch().uint8) if nbytes else None
+
+
+def _prompt_shape(q, v):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k must be [B, T, H, D] and v [B, T, H, M]")
+    return (*q.shape, v.shape[3])
 
 
 def linattn_decay_forward(q, k, v, log_decay, state=None, *, scale=1.0, lengths=None, want_state=False, out=None,
@@ -408,20 +416,33 @@ def linattn_decay_forward(q, k, v, log_decay, state=None, *, scale=1.0, lengths=
     number of positions (``lengths`` [B] int32, or T for all; out is zero behind them).  Returns
     (out [B, T, H, M], the state after each row's last position or None)."""
     torch = _torch()
-    with _scope(q, stream):
-        B, T, H, D, M, dt = _check_decay(q, k, v, log_decay, lengths, state=state)
-        if out is None:
-            out = torch.empty((B, T, H, M), dtype=q.dtype, device=q.device)
-        else:
-            _check_heads(q, (B, T, H, M), q.dtype, out=out)
-        s_out = torch.empty((B, H, D, M), dtype=torch.float32, device=q.device) if want_state else None
-        abi = _abi()
-        need = abi.linattn_decay_workspace_size(LINATTN_OP_FORWARD, B, T, H, D, M, dt)
-        ws = _scratch(need, q.device)
-        abi.check(abi.linattn_decay_forward(B, T, H, D, M, dt, _view4(q), _view4(k), _view4(v), _ptr(log_decay),
-                                            scale, _ptr(lengths), _ptr(state), _view4(out), _ptr(s_out), _ptr(ws),
-                                            need, _status_ptr(q.device),
-                                            torch.cuda.current_stream(q.device).cuda_stream))
+    dev, current = _on_device(q)
+    if stream is not None or not current:
+        with _scope(q, stream):
+            return linattn_decay_forward(q, k, v, log_decay, state, scale=scale, lengths=lengths,
+                                         want_state=want_state, out=out)
+    B, T, H, D, M = _prompt_shape(q, v)
+    dtype, f32 = q.dtype, torch.float32
+    dt = _dtype_code(q)
+    at = []
+    _head_view(at, "q", q, dev, dtype, (B, T, H, D))
+    _head_view(at, "k", k, dev, dtype, (B, T, H, D))
+    _head_view(at, "v", v, dev, dtype, (B, T, H, M))
+    if out is None:
+        out = q.new_empty((B, T, H, M))
+    _head_view(at, "out", out, dev, dtype, (B, T, H, M))
+    g = _plain_ptr("log_decay", log_decay, dev, f32, (H,))
+    n = _plain_ptr("lengths", lengths, dev, torch.int32, (B,))
+    s_in = _plain_ptr("state", state, dev, f32, (B, H, D, M))
+    s_out = q.new_empty((B, H, D, M), dtype=f32) if want_state else None
+    need = _decay_need(dev, LINATTN_OP_FORWARD, B, T, H, D, M, dt)
+    ws = _scratch(q, need)
+    at = array.array("q", at)
+    w, abi = at.buffer_info()[0], _abi()
+    rc = abi.linattn_decay_forward_at(B, T, H, D, M, dt, w, w + 32, w + 64, g, scale, n, s_in, w + 96, _ptr(s_out),
+                                      _ptr(ws), need, _status_ptr(q, dev), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        abi.check(rc)
     return out, s_out
 
 
@@ -431,24 +452,41 @@ def linattn_decay_backward(q, k, v, log_decay, grad_out, state=None, *, scale=1.
     arguments, given grad_out = dL/dout and, optionally, ``grad_state_out`` = dL/d(state after the last
     position); grad_state is dL/dstate.  log_decay is a constant."""
     torch = _torch()
-    with _scope(q, stream):
-        B, T, H, D, M, dt = _check_decay(q, k, v, log_decay, lengths, state=state, grad_state_out=grad_state_out)
-        _check_heads(q, (B, T, H, M), q.dtype, grad_out=grad_out)
-        new = lambda n: torch.empty((B, T, H, n), dtype=q.dtype, device=q.device)  # noqa: E731
-        grad_q = new(D) if grad_q is None else grad_q
-        grad_k = new(D) if grad_k is None else grad_k
-        grad_v = new(M) if grad_v is None else grad_v
-        _check_heads(q, (B, T, H, D), q.dtype, grad_q=grad_q, grad_k=grad_k)
-        _check_heads(q, (B, T, H, M), q.dtype, grad_v=grad_v)
-        gs = torch.empty((B, H, D, M), dtype=torch.float32, device=q.device) if want_grad_state else None
-        abi = _abi()
-        need = abi.linattn_decay_workspace_size(LINATTN_OP_BACKWARD, B, T, H, D, M, dt)
-        ws = _scratch(need, q.device)
-        abi.check(abi.linattn_decay_backward(B, T, H, D, M, dt, _view4(q), _view4(k), _view4(v), _ptr(log_decay),
-                                             scale, _ptr(lengths), _ptr(state), _view4(grad_out),
-                                             _ptr(grad_state_out), _view4(grad_q), _view4(grad_k), _view4(grad_v),
-                                             _ptr(gs), _ptr(ws), need, _status_ptr(q.device),
-                                             torch.cuda.current_stream(q.device).cuda_stream))
+    dev, current = _on_device(q)
+    if stream is not None or not current:
+        with _scope(q, stream):
+            return linattn_decay_backward(q, k, v, log_decay, grad_out, state, scale=scale, lengths=lengths,
+                                          grad_state_out=grad_state_out, want_grad_state=want_grad_state,
+                                          grad_q=grad_q, grad_k=grad_k, grad_v=grad_v)
+    B, T, H, D, M = _prompt_shape(q, v)
+    dtype, f32 = q.dtype, torch.float32
+    dt = _dtype_code(q)
+    wide_d, wide_m = (B, T, H, D), (B, T, H, M)
+    at = []
+    _head_view(at, "q", q, dev, dtype, wide_d)
+    _head_view(at, "k", k, dev, dtype, wide_d)
+    _head_view(at, "v", v, dev, dtype, wide_m)
+    _head_view(at, "grad_out", grad_out, dev, dtype, wide_m)
+    grad_q = q.new_empty(wide_d) if grad_q is None else grad_q
+    grad_k = q.new_empty(wide_d) if grad_k is None else grad_k
+    grad_v = q.new_empty(wide_m) if grad_v is None else grad_v
+    _head_view(at, "grad_q", grad_q, dev, dtype, wide_d)
+    _head_view(at, "grad_k", grad_k, dev, dtype, wide_d)
+    _head_view(at, "grad_v", grad_v, dev, dtype, wide_m)
+    g = _plain_ptr("log_decay", log_decay, dev, f32, (H,))
+    n = _plain_ptr("lengths", lengths, dev, torch.int32, (B,))
+    s_in = _plain_ptr("state", state, dev, f32, (B, H, D, M))
+    gs_out = _plain_ptr("grad_state_out", grad_state_out, dev, f32, (B, H, D, M))
+    gs = q.new_empty((B, H, D, M), dtype=f32) if want_grad_state else None
+    need = _decay_need(dev, LINATTN_OP_BACKWARD, B, T, H, D, M, dt)
+    ws = _scratch(q, need)
+    at = array.array("q", at)
+    w, abi = at.buffer_info()[0], _abi()
+    rc = abi.linattn_decay_backward_at(B, T, H, D, M, dt, w, w + 32, w + 64, g, scale, n, s_in, w + 96, gs_out, w + 128,
+                                       w + 160, w + 192, _ptr(gs), _ptr(ws), need, _status_ptr(q, dev),
+                                       torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        abi.check(rc)
     return grad_q, grad_k, grad_v, gs
 
 
@@ -456,27 +494,33 @@ def linattn_decay_step(q, k, v, log_decay, state, *, scale=1.0, out=None, state_
     """One token for N sequences: q, k [N, H, D], v [N, H, M], state [N, H, D, M] float32.  ``state_out``
     defaults to updating ``state`` in place.  Returns (out [N, H, M], state_out)."""
     torch = _torch()
-    with _scope(q, stream):
-        if q.dim() != 3 or v.dim() != 3:
-            raise ValueError("q, k must be [N, H, D] and v [N, H, M]")
-        N, H, D = q.shape
-        M = v.shape[2]
-        _check_heads(q, q.shape, q.dtype, q=q, k=k)
-        _check_heads(q, (N, H, M), q.dtype, v=v)
-        if out is None:
-            out = torch.empty((N, H, M), dtype=q.dtype, device=q.device)
-        else:
-            _check_heads(q, (N, H, M), q.dtype, out=out)
-        if state_out is None:
-            state_out = state
-        f32 = torch.float32
-        _check_plain(q, log_decay=(log_decay, (H,), f32), state=(state, (N, H, D, M), f32),
-                     state_out=(state_out, (N, H, D, M), f32))
-        abi = _abi()
-        view = lambda t: abi.View(t.data_ptr(), t.stride(0), 0, t.stride(1))  # noqa: E731
-        abi.check(abi.linattn_decay_step(N, H, D, M, _dtype_code(q), view(q), view(k), view(v), _ptr(log_decay),
-                                         scale, _ptr(state), view(out), _ptr(state_out),
-                                         torch.cuda.current_stream(q.device).cuda_stream))
+    dev, current = _on_device(q)
+    if stream is not None or not current:
+        with _scope(q, stream):
+            return linattn_decay_step(q, k, v, log_decay, state, scale=scale, out=out, state_out=state_out)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k must be [N, H, D] and v [N, H, M]")
+    N, H, D = q.shape
+    M = v.shape[2]
+    dtype, f32 = q.dtype, torch.float32
+    at = []
+    _head_view(at, "q", q, dev, dtype, (N, H, D))
+    _head_view(at, "k", k, dev, dtype, (N, H, D))
+    _head_view(at, "v", v, dev, dtype, (N, H, M))
+    if out is None:
+        out = q.new_empty((N, H, M))
+    _head_view(at, "out", out, dev, dtype, (N, H, M))
+    g = _plain_ptr("log_decay", log_decay, dev, f32, (H,))
+    s_in = _plain_ptr("state", state, dev, f32, (N, H, D, M))
+    if state_out is None:
+        state_out = state
+    s_out = s_in if state_out is state else _plain_ptr("state_out", state_out, dev, f32, (N, H, D, M))
+    at = array.array("q", at)
+    w, abi = at.buffer_info()[0], _abi()
+    rc = abi.linattn_decay_step_at(N, H, D, M, _dtype_code(q), w, w + 32, w + 64, g, scale, s_in, w + 96, s_out,
+                                   torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        abi.check(rc)
     return out, state_out
 
 
@@ -581,39 +625,47 @@ def linattn_rotary(q, k, positions, inv_freq, *, mscale=1.0, interleaved=False, 
     ``rotary_frequencies``); pairs are (i, i + R/2), or (2i, 2i + 1) if ``interleaved``.  ``inverse``
     rotates back.  ``out_q`` / ``out_k`` may be q / k (in place).  Returns (out_q, out_k)."""
     torch = _torch()
-    with _scope(q, stream):
-        if q.dim() != 4 or (k is not None and k.dim() != 4):
-            raise ValueError("q and k must be [B, T, heads, D]")
-        B, T, Hq, D = q.shape
-        Hk = 0 if k is None else k.shape[2]
-        if positions.dtype not in (torch.int32, torch.int64) or tuple(positions.shape) not in ((T,), (B, T)):
-            raise ValueError("positions must be int32 or int64, [T] or [B, T]")
-        if positions.device != q.device or (T > 1 and positions.stride(-1) != 1):
-            raise ValueError("positions must be on q's device, contiguous along T")
-        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
-            raise ValueError("inv_freq must be a float64 vector")
-        R = 2 * inv_freq.shape[0]
-        _check_plain(q, inv_freq=(inv_freq, inv_freq.shape, torch.float64))
-        _check_heads(q, q.shape, q.dtype, q=q)
-        if out_q is None:
-            out_q = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device)
-        else:
-            _check_heads(q, q.shape, q.dtype, out_q=out_q)
-        if k is not None:
-            _check_heads(q, (B, T, Hk, D), q.dtype, k=k)
-            if out_k is None:
-                out_k = torch.empty((B, T, Hk, D), dtype=q.dtype, device=q.device)
-            else:
-                _check_heads(q, k.shape, q.dtype, out_k=out_k)
-        elif out_k is not None:
-            raise ValueError("out_k without k")
-        abi = _abi()
-        abi.check(abi.linattn_rotary(B, T, D, R, _dtype_code(q), Hq, _view4(q), Hk,
-                                     None if k is None else _view4(k), positions.data_ptr(),
-                                     positions.element_size(), positions.stride(0) if positions.dim() == 2 else 0,
-                                     inv_freq.data_ptr(), mscale, int(interleaved), int(inverse), _view4(out_q),
-                                     None if k is None else _view4(out_k),
-                                     torch.cuda.current_stream(q.device).cuda_stream))
+    dev, current = _on_device(q)
+    if stream is not None or not current:
+        with _scope(q, stream):
+            return linattn_rotary(q, k, positions, inv_freq, mscale=mscale, interleaved=interleaved, inverse=inverse,
+                                  out_q=out_q, out_k=out_k)
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be [B, T, heads, D]")
+    dtype, shape = q.dtype, q.shape
+    B, T, Hq, D = shape
+    if positions.dtype not in (torch.int32, torch.int64) or positions.shape not in ((T,), (B, T)):
+        raise ValueError("positions must be int32 or int64, [T] or [B, T]")
+    p_stride = positions.stride()
+    if positions.get_device() != dev or (T > 1 and p_stride[-1] != 1):
+        raise ValueError("positions must be on q's device, contiguous along T")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a float64 vector")
+    pairs = inv_freq.shape[0]
+    f = _plain_ptr("inv_freq", inv_freq, dev, torch.float64, (pairs,))
+    at = []
+    _head_view(at, "q", q, dev, dtype, shape)
+    if out_q is None:
+        out_q = q.new_empty(shape)
+    _head_view(at, "out_q", out_q, dev, dtype, shape)
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[2]
+        k_shape = (B, T, Hk, D)
+        _head_view(at, "k", k, dev, dtype, k_shape)
+        if out_k is None:
+            out_k = q.new_empty(k_shape)
+        _head_view(at, "out_k", out_k, dev, dtype, k_shape)
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    at = array.array("q", at)
+    w, abi = at.buffer_info()[0], _abi()
+    rc = abi.linattn_rotary_at(B, T, D, 2 * pairs, _dtype_code(q), Hq, w, Hk, w + 64 if Hk else None,
+                               positions.data_ptr(), positions.element_size(),
+                               p_stride[0] if len(p_stride) == 2 else 0, f, mscale, interleaved, inverse, w + 32,
+                               w + 96 if Hk else None, torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        abi.check(rc)
     return out_q, out_k
 
 

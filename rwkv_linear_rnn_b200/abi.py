@@ -102,6 +102,21 @@ for _name, (_res, _args) in _SIGS.items():
     _fn.argtypes = _args
 
 
+def _by_address(name):
+    """The C function with its linattn_view arguments given as addresses (ints): the tensor helpers pack a
+    call's views into one array('q') instead of a ctypes structure each."""
+    fn = lib[name]  # a function object of its own
+    fn.restype, args = _SIGS[name]
+    fn.argtypes = [_p if a is _view else a for a in args]
+    return fn
+
+
+linattn_decay_forward_at = _by_address("linattn_decay_forward")
+linattn_decay_backward_at = _by_address("linattn_decay_backward")
+linattn_decay_step_at = _by_address("linattn_decay_step")
+linattn_rotary_at = _by_address("linattn_rotary")
+
+
 class WKVError(RuntimeError):
     def __init__(self, status: int):
         self.status = status

@@ -57,6 +57,13 @@ struct Pass {
   int32_t *status;
 };
 
+// Passes of one call that are launched together (blockIdx.y): they have the
+// same positions and segments, and sizes of one class.
+struct Group {
+  Pass p[3];
+  int n;
+};
+
 // Positions of row b.
 __device__ __forceinline__ int64_t row_len(const Pass &p, int64_t b) {
   if (!p.lengths) return p.T;
@@ -79,15 +86,19 @@ __device__ __forceinline__ Decay decay_of(float g, int64_t n) {
 }
 __device__ __forceinline__ float decayed(float x, Decay d) { return fmaf(x, d.m, d.near_one ? x : 0.f); }
 
-// Launches.  Each returns the first launch's failure.
-cudaError_t launch_rec(const Pass &p, int dtype, bool sums_only, cudaStream_t st);
-cudaError_t launch_scan(const Pass &p, cudaStream_t st);
-// The tensor-core pass (bfloat16): whether it can take the views, its segments
-// per head and their length, and its launches.
+// Launches.  Each returns the first launch's failure.  X of one rec_class may
+// share a launch; rec_segments are the segments per head for `npass` passes.
+int rec_class(int X);
+int64_t rec_segments(int64_t BH, int64_t T, int X, int Y, int npass, int sms);
+cudaError_t launch_rec(const Group &g, int dtype, bool sums_only, cudaStream_t st);
+cudaError_t launch_scan(const Group &g, cudaStream_t st);
+// The tensor-core passes (bfloat16): whether one can take the views, whether
+// sizes share a launch, the segments per head and their length, the launches.
 bool tc_fits(const Pass &p);
-int64_t tc_segments(int64_t BH, int64_t T, int sms);
+inline bool tc_one_class(int D, int M) { return (D <= 64) == (M <= 64); }
+int64_t tc_segments(int64_t BH, int64_t T, int npass, int sms);
 int64_t tc_segment_len(int64_t T, int64_t nseg);
-cudaError_t launch_tc(const Pass &p, bool sums_only, cudaStream_t st);
+cudaError_t launch_tc(const Group &g, bool sums_only, cudaStream_t st);
 struct StepArgs {
   int64_t N, H;
   int D, M;

@@ -68,16 +68,6 @@ bool overlap(const void *a, const void *b, size_t bytes) {
 
 View view(const linattn_view *v) { return View{v->ptr, v->stride_b, v->stride_t, v->stride_h}; }
 
-// Segments per head of the recurrence kernel.  One head's segment is a chain
-// of dependent positions run by Y / 16 warps; below about two warps per
-// scheduler the chain's latency shows, so heads are split until there are
-// that many, down to 64 positions per segment (the sums' pass and the scan
-// cost about 2/3 of an output pass, and each segment one state of traffic).
-int64_t rec_segments(int64_t BH, int64_t T, int Y, int sms) {
-  const int64_t warps = BH * ((Y + 15) / 16), want = 8 * (int64_t)sms;
-  if (warps * 2 >= want) return 1;
-  return std::max<int64_t>(1, std::min((want + warps - 1) / warps, T / 64));
-}
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t seg_bytes(const Dims &d, int64_t nseg) { return nseg > 1 ? up256(sizeof(float) * d.B * d.H * nseg * d.D * d.M) : 0; }
 
@@ -85,41 +75,58 @@ size_t seg_bytes(const Dims &d, int64_t nseg) { return nseg > 1 ? up256(sizeof(f
 // Up to 32 positions a chunk of 128 is mostly padding.
 bool uses_tc(const Dims &d) { return d.dtype == WKV_BF16 && d.T > 32 && d.D % 8 == 0 && d.M % 8 == 0; }
 
-// Bytes that the passes of one call need: they run one after the other and
-// share one buffer.
-size_t pass_bytes(const Dims &d, int Y) {
+// Bytes of the segments' states of `n` passes of X x Y launched together.
+size_t group_bytes(const Dims &d, int X, int Y, int n) {
   const int64_t BH = d.B * d.H;
-  const size_t rec = seg_bytes(d, rec_segments(BH, d.T, Y, num_sms()));
-  return uses_tc(d) ? std::max(rec, seg_bytes(d, tc_segments(BH, d.T, num_sms()))) : rec;
+  const size_t rec = seg_bytes(d, rec_segments(BH, d.T, X, Y, n, num_sms()));
+  return n * (uses_tc(d) ? std::max(rec, seg_bytes(d, tc_segments(BH, d.T, n, num_sms()))) : rec);
 }
+// Groups run one after the other and share the workspace.  A backward's
+// passes are one group or, with heads of two classes, {grad_q, grad_k} and
+// {grad_v}.
 size_t workspace(int op, const Dims &d) {
-  const size_t f = pass_bytes(d, d.M);
-  return op == LINATTN_OP_FORWARD ? f : std::max(f, pass_bytes(d, d.D));
+  if (op == LINATTN_OP_FORWARD) return group_bytes(d, d.D, d.M, 1);
+  const int x = std::max(d.D, d.M);
+  return std::max({group_bytes(d, x, x, 3), group_bytes(d, d.M, d.D, 2), group_bytes(d, d.D, d.M, 1)});
 }
 int check_ws(size_t need, const void *ws, size_t bytes) {
   if (need == 0) return WKV_OK;
   return !ws || !aligned(ws, 256) || bytes < need ? WKV_ERR_WORKSPACE : WKV_OK;
 }
 
-// One pass: segment sums and their scan if the heads are split, then the
-// outputs.
-cudaError_t run_pass(Pass p, const Dims &d, void *ws, cudaStream_t st) {
-  p.seg = static_cast<float *>(ws);
-  const bool tc = uses_tc(d) && tc_fits(p);
-  if (tc) {
-    p.nseg = (int)tc_segments(d.B * d.H, d.T, num_sms());
-    p.seg_len = tc_segment_len(d.T, p.nseg);
-  } else {
-    p.nseg = (int)rec_segments(d.B * d.H, d.T, p.Y, num_sms());
-    p.seg_len = (p.T + p.nseg - 1) / p.nseg;
+// The passes of a group: segment sums and their scan if the heads are split,
+// then the outputs.
+cudaError_t run_group(Group &g, const Dims &d, bool tc, void *ws, cudaStream_t st) {
+  int X = 0, Y = 0;
+  for (int i = 0; i < g.n; ++i) X = std::max(X, g.p[i].X), Y = std::max(Y, g.p[i].Y);
+  const int64_t BH = d.B * d.H;
+  const int64_t nseg = tc ? tc_segments(BH, d.T, g.n, num_sms()) : rec_segments(BH, d.T, X, Y, g.n, num_sms());
+  for (int i = 0; i < g.n; ++i) {
+    Pass &p = g.p[i];
+    p.nseg = (int)nseg;
+    p.seg_len = tc ? tc_segment_len(d.T, nseg) : (d.T + nseg - 1) / nseg;
+    p.seg = static_cast<float *>(ws) + i * (seg_bytes(d, nseg) / sizeof(float));
   }
-  auto launch = [&](bool sums_only) { return tc ? launch_tc(p, sums_only, st) : launch_rec(p, d.dtype, sums_only, st); };
+  auto launch = [&](bool sums_only) { return tc ? launch_tc(g, sums_only, st) : launch_rec(g, d.dtype, sums_only, st); };
   cudaError_t e = cudaSuccess;
-  if (p.nseg > 1) {
+  if (nseg > 1) {
     e = launch(true);
-    if (e == cudaSuccess) e = launch_scan(p, st);
+    if (e == cudaSuccess) e = launch_scan(g, st);
   }
   return e == cudaSuccess ? launch(false) : e;
+}
+cudaError_t run_passes(const Pass *p, int n, const Dims &d, void *ws, cudaStream_t st) {
+  bool tc = uses_tc(d);
+  for (int i = 0; i < n; ++i) tc = tc && tc_fits(p[i]);
+  const bool one = tc ? tc_one_class(d.D, d.M) : rec_class(d.D) == rec_class(d.M);
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < n && e == cudaSuccess;) {
+    Group g{};
+    const int X = p[i].X;
+    while (i < n && (one || p[i].X == X)) g.p[g.n++] = p[i++];
+    e = run_group(g, d, tc, ws, st);
+  }
+  return e;
 }
 
 // T = 0, or no work at all: the state goes through.
@@ -163,7 +170,7 @@ extern "C" int linattn_decay_forward(int64_t B, int64_t T, int64_t H, int D, int
   p.a = view(q), p.b = view(k), p.c = view(v), p.o = view(out);
   p.log_decay = log_decay, p.lengths = lengths, p.s_in = state_in, p.s_out = state_out, p.exact_state = 1;
   p.si = scale, p.sk = 1.f, p.status = status;
-  return rc_of(run_pass(p, d, ws, st));
+  return rc_of(run_passes(&p, 1, d, ws, st));
 }
 
 extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, int M, int dtype, const linattn_view *q,
@@ -200,26 +207,27 @@ extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, in
   if (rc != WKV_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T == 0) return pass_state_through(d, grad_state_out, grad_state_in, st);
-  Pass p{};
-  p.B = B, p.T = T, p.H = H;
-  p.log_decay = log_decay, p.lengths = lengths, p.status = status;
+  Pass p[3]{};
+  for (Pass &x : p) {
+    x.B = B, x.T = T, x.H = H;
+    x.log_decay = log_decay, x.lengths = lengths, x.status = status;
+  }
   // grad_q: forward in time, the state transposed
-  p.X = M, p.Y = D;
-  p.a = view(grad_out), p.b = view(v), p.c = view(k), p.o = view(grad_q);
-  p.s_in = state_in, p.s_in_t = 1;
-  p.si = scale, p.sk = 1.f;
-  cudaError_t e = run_pass(p, d, ws, st);
+  p[0].X = M, p[0].Y = D;
+  p[0].a = view(grad_out), p[0].b = view(v), p[0].c = view(k), p[0].o = view(grad_q);
+  p[0].s_in = state_in, p[0].s_in_t = 1;
+  p[0].si = scale, p[0].sk = 1.f;
   // grad_k: reverse, the state's adjoint transposed
-  p.a = view(v), p.b = view(grad_out), p.c = view(q), p.o = view(grad_k);
-  p.s_in = grad_state_out;
-  p.si = 1.f, p.sk = scale, p.reverse = 1;
-  if (e == cudaSuccess) e = run_pass(p, d, ws, st);
+  p[1].X = M, p[1].Y = D;
+  p[1].a = view(v), p[1].b = view(grad_out), p[1].c = view(q), p[1].o = view(grad_k);
+  p[1].s_in = grad_state_out, p[1].s_in_t = 1;
+  p[1].si = 1.f, p[1].sk = scale, p[1].reverse = 1;
   // grad_v and the gradient of the state handed in
-  p.X = D, p.Y = M;
-  p.a = view(k), p.b = view(q), p.c = view(grad_out), p.o = view(grad_v);
-  p.s_in_t = 0, p.s_out = grad_state_in, p.exact_state = 1;
-  if (e == cudaSuccess) e = run_pass(p, d, ws, st);
-  return rc_of(e);
+  p[2].X = D, p[2].Y = M;
+  p[2].a = view(k), p[2].b = view(q), p[2].c = view(grad_out), p[2].o = view(grad_v);
+  p[2].s_in = grad_state_out, p[2].s_out = grad_state_in, p[2].exact_state = 1;
+  p[2].si = 1.f, p[2].sk = scale, p[2].reverse = 1;
+  return rc_of(run_passes(p, 3, d, ws, st));
 }
 
 extern "C" int linattn_decay_step(int64_t N, int64_t H, int D, int M, int dtype, const linattn_view *q,

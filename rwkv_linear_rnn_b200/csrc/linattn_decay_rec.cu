@@ -2,17 +2,24 @@
 // CUDA cores: the recurrence itself, the single-token step, and the scan that
 // joins the segments of a long sequence.
 //
-// The recurrence R_t = lam R_{t-1} + b_t c_t^T, o_t = a_t^T R_t costs three
-// FMAs per state element and position (the two of the update, one of the
-// product), so it is bound by the FMA pipes: it serves float32 tensors (which
-// the tensor cores' bfloat16 products would round), heads and strides that
-// TMA cannot describe, and sequences of a few positions.
+// The recurrence R_t = lam R_{t-1} + b_t c_t^T, o_t = a_t^T R_t costs two FMAs
+// per state element and position and the decay.  The decay leaves the inner
+// loop: over a batch of 8 positions the kernel holds R / lam^k instead of R
+// (b enters divided by lam^k, o is multiplied by it: scalings, which round no
+// more than the products they replace) and multiplies R by lam^8 once.  Where
+// lam^8 < 2^-16 that would cost range, and R is multiplied at each position.
 //
-// Layout: a warp owns 16 columns of Y and all rows of X; lane (xl, yl) =
-// (lane / 4, lane % 4) holds rows xl * RX .. + RX - 1 of columns
-// 4 yl .. + 3, so a state row is read as 64-byte segments, a and b come from
-// shared memory as broadcast float4s, and the product needs one reduction
-// over the 8 lanes that share columns: 4 shuffles and no block barrier.
+// The kernel is bound by the FMA pipes: it serves float32 tensors (which the
+// tensor cores' bfloat16 products would round), heads and strides that TMA
+// cannot describe, and sequences of a few positions.
+//
+// Layout: a warp owns 64 rows (32 if X <= 32) and 32 columns of the state;
+// lane (lane / 8, lane % 8) holds 4 columns of 16 (8) rows, as pairs of rows
+// for the two-wide FMAs.  Per position a lane reads a and b of its rows as
+// float4s that 8 lanes share and its 4 columns of c: 9 loads for 128 FMAs.
+// The products' sums over the 4 lanes of a column are taken for four
+// positions at a time (12 shuffles, one float4 stored), over the two warps of
+// a column's rows when they are written out.
 #include <algorithm>
 
 #include "linattn_decay.cuh"
@@ -20,8 +27,8 @@
 namespace wkv {
 namespace decay {
 
-constexpr int kTB = 16;     // positions staged in shared memory at a time
-constexpr int kRecWarps = 8;  // most warps per block: 128 columns of Y
+constexpr int kTB = 16;       // positions staged in shared memory at a time
+constexpr int kStepWarps = 8; // most warps per block of the step: 128 columns
 
 template <typename E>
 __device__ __forceinline__ float load1(const void *p, int64_t i);
@@ -44,6 +51,310 @@ __device__ __forceinline__ void store1<uint16_t>(const void *p, int64_t i, float
   unsigned short h;
   asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(x));
   static_cast<uint16_t *>(const_cast<void *>(p))[i] = h;
+}
+
+// ------------------------------------------------------ two-wide float32 ---
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 both(float x) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(x));
+  return d;
+}
+__device__ __forceinline__ f2 pair(float x, float y) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(f2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
+// Batches of 8 positions are taken relative to their start unless lam^8 is
+// below 2^-16.
+constexpr int kBatch = 8;
+constexpr float kSlowest = -16.f * 0.69314718f / kBatch;
+
+// One pass of the recurrence over a segment of a head (blockIdx.x: head and
+// segment, blockIdx.y: pass).  OUT: outputs, from the segment's start state;
+// otherwise the segment's sum alone, from zero.  VEC: float32 in 16-byte
+// pieces, fetched one batch ahead.
+template <typename E, int TX, bool OUT, bool VEC>
+__global__ void __launch_bounds__(256) rec_kernel(const __grid_constant__ Group g, int nx, int nwy) {
+  const Pass &p = g.p[blockIdx.y];
+  extern __shared__ __align__(16) float rec_smem[];
+  constexpr int QX = TX / 4;  // a lane's float4s of rows, 16 rows apart
+  const int XS = 4 * TX * nx, YS = 32 * nwy;
+  constexpr int NBUF = VEC ? 2 : 1;
+  float *sb = rec_smem, *sc = sb + NBUF * kTB * XS, *sa = sc + NBUF * kTB * YS;  // sa, so: OUT only
+  float *so = sa + NBUF * kTB * XS;                                           // [nx][kTB][YS]
+  __shared__ float wk[kBatch], uk[kBatch];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wx = warp % nx;
+  const int rg = lane >> 3, x0 = 4 * TX * wx + 4 * rg, y0 = 32 * (warp / nx) + 4 * (lane & 7);
+  const int64_t bh = blockIdx.x / p.nseg, sg = blockIdx.x % p.nseg;
+  const int64_t b = bh / p.H, h = bh % p.H;
+  const int64_t n = row_len(p, b);
+  const int64_t t0 = sg * p.seg_len, tz = min(t0 + p.seg_len, p.T), t1 = max(t0, min(tz, n));
+  const float gd = p.log_decay[h];
+  const bool slow = !(gd >= kSlowest);
+  const E *pa = static_cast<const E *>(p.a.p) + (b * p.a.sb + h * p.a.sh),
+          *pb = static_cast<const E *>(p.b.p) + (b * p.b.sb + h * p.b.sh),
+          *pc = static_cast<const E *>(p.c.p) + (b * p.c.sb + h * p.c.sh);
+  E *po = static_cast<E *>(const_cast<void *>(p.o.p)) + (b * p.o.sb + h * p.o.sh);
+  const int64_t XY = (int64_t)p.X * p.Y;
+  const int64_t count = t1 - t0, step = p.reverse ? -1 : 1;
+  const int64_t t_first = p.reverse ? t1 - 1 : t0;  // row i of the segment is position t_first + step i
+
+  if (tid < kBatch) {  // reverse: the state handed in meets the first position undecayed
+    const float e = slow ? 0.f : gd * (float)(tid + (p.reverse ? 0 : 1));
+    wk[tid] = p.sk * expf(-e);
+    uk[tid] = p.si * expf(e);
+  }
+
+  // rows 16 q + x0 + (0..3), as two pairs each
+  f2 S[2 * QX][4];
+  const float *s0 = !OUT ? nullptr : p.nseg > 1 ? p.seg + blockIdx.x * XY : p.s_in ? p.s_in + bh * XY : nullptr;
+  const bool s0_t = p.nseg == 1 && p.s_in_t;
+#pragma unroll
+  for (int r = 0; r < 2 * QX; ++r) {
+    float v[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int x = x0 + 16 * (r >> 1) + 2 * (r & 1) + i;
+      if (s0 && !s0_t && (p.Y & 3) == 0 && x < p.X && y0 < p.Y) {
+        const float4 f = __ldcs(reinterpret_cast<const float4 *>(s0 + (int64_t)x * p.Y + y0));
+        v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[i][e] = s0 && x < p.X && y0 + e < p.Y ? s0[s0_t ? (int64_t)(y0 + e) * p.X + x : (int64_t)x * p.Y + y0 + e] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[r][e] = pair(v[0][e], v[1][e]);
+  }
+  auto decay = [&](Decay d) {
+    const f2 m = both(d.m);
+    if (d.near_one) {
+#pragma unroll
+      for (int r = 0; r < 2 * QX; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[r][e] = fma2(S[r][e], m, S[r][e]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2 * QX; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[r][e] = mul2(S[r][e], m);
+    }
+  };
+  const Decay lam = decay_of(gd, 1), lam_batch = decay_of(gd, kBatch);
+
+  // rows s.. of the segment (m of them) into buffer `buf`
+  auto fetch = [&](int64_t s, int m, int buf) {
+    float *db = sb + buf * kTB * XS, *dc = sc + buf * kTB * YS, *da = sa + buf * kTB * XS;
+    const int64_t t = t_first + step * s;
+    if constexpr (VEC) {
+      const int ux = XS / 4, uy = YS / 4;
+      for (int e = tid; e < m * ux; e += blockDim.x) {
+        const int i = e / ux, x = 4 * (e % ux);
+        const bool real = x < p.X;
+        cp_async16(smem_addr(db + 4 * e), pb + (t + step * i) * p.b.st + (real ? x : 0), real);
+        if (OUT) cp_async16(smem_addr(da + 4 * e), pa + (t + step * i) * p.a.st + (real ? x : 0), real);
+      }
+      for (int e = tid; e < m * uy; e += blockDim.x) {
+        const int i = e / uy, y = 4 * (e % uy);
+        const bool real = y < p.Y;
+        cp_async16(smem_addr(dc + 4 * e), pc + (t + step * i) * p.c.st + (real ? y : 0), real);
+      }
+    } else {
+      for (int e = tid; e < m * XS; e += blockDim.x) {
+        const int i = e / XS, x = e % XS;
+        db[e] = x < p.X ? load1<E>(pb, (t + step * i) * p.b.st + x) : 0.f;
+        if (OUT) da[e] = x < p.X ? load1<E>(pa, (t + step * i) * p.a.st + x) : 0.f;
+      }
+      for (int e = tid; e < m * YS; e += blockDim.x) {
+        const int i = e / YS, y = e % YS;
+        dc[e] = y < p.Y ? load1<E>(pc, (t + step * i) * p.c.st + y) : 0.f;
+      }
+    }
+  };
+
+  int buf = 0;
+  if (VEC && count > 0) {
+    fetch(0, (int)min((int64_t)kTB, count), 0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  for (int64_t s = 0; s < count; s += kTB) {
+    const int m = (int)min((int64_t)kTB, count - s);
+    if constexpr (VEC) {
+      if (s + kTB < count) fetch(s + kTB, (int)min((int64_t)kTB, count - s - kTB), buf ^ 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      fetch(s, m, 0);
+    }
+    __syncthreads();
+    const float *cb = sb + buf * kTB * XS + x0, *cc = sc + buf * kTB * YS + y0, *ca = sa + buf * kTB * XS + x0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < m; i0 += 4) {
+      f2 y[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[k][e] = 0ull;
+        const int i = i0 + k;
+        if (i >= m) continue;
+        if (slow && !p.reverse) decay(lam);
+        const float w = wk[i & (kBatch - 1)];
+        const float4 cv = *reinterpret_cast<const float4 *>(cc + i * YS);
+        const f2 c[4] = {both(cv.x * w), both(cv.y * w), both(cv.z * w), both(cv.w * w)};
+#pragma unroll
+        for (int q = 0; q < QX; ++q) {
+          const ulonglong2 bv = *reinterpret_cast<const ulonglong2 *>(cb + i * XS + 16 * q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            S[2 * q][e] = fma2(bv.x, c[e], S[2 * q][e]);
+            S[2 * q + 1][e] = fma2(bv.y, c[e], S[2 * q + 1][e]);
+          }
+          if (OUT) {
+            const ulonglong2 av = *reinterpret_cast<const ulonglong2 *>(ca + i * XS + 16 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[k][e] = fma2(av.x, S[2 * q][e], y[k][e]);
+              y[k][e] = fma2(av.y, S[2 * q + 1][e], y[k][e]);
+            }
+          }
+        }
+        if (slow && p.reverse) decay(lam);
+      }
+      if (OUT) {
+        // 16 sums over the lanes rg = 0..3: lane rg ends with those of position i0 + rg
+        float z[8], o[4];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 lo = unpair(y[e >> 2][e & 3]), hi = unpair(y[2 + (e >> 2)][e & 3]);
+          const float l = lo.x + lo.y, u = hi.x + hi.y;
+          z[e] = (rg & 2 ? u : l) + __shfl_xor_sync(~0u, rg & 2 ? l : u, 16);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = (rg & 1 ? z[4 + e] : z[e]) + __shfl_xor_sync(~0u, rg & 1 ? z[e] : z[4 + e], 8);
+        const float u = uk[(i0 + rg) & (kBatch - 1)];
+        *reinterpret_cast<float4 *>(so + (wx * kTB + i0 + rg) * YS + y0) = make_float4(u * o[0], u * o[1], u * o[2], u * o[3]);
+      }
+      if (!slow) {
+        if (i0 + 4 >= m) {
+          const int k = m & (kBatch - 1);
+          decay(k == 0 ? lam_batch : decay_of(gd, k));
+        } else if ((i0 & (kBatch - 1)) == kBatch - 4) {
+          decay(lam_batch);
+        }
+      }
+    }
+    __syncthreads();
+    if (OUT) {
+      const int64_t t = t_first + step * s;
+      if constexpr (VEC) {
+        const int uy = p.Y / 4;
+        for (int e = tid; e < m * uy; e += blockDim.x) {
+          const int i = e / uy, yy = 4 * (e % uy);
+          float4 v = *reinterpret_cast<const float4 *>(so + i * YS + yy);
+          if (nx == 2) {
+            const float4 u = *reinterpret_cast<const float4 *>(so + (kTB + i) * YS + yy);
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+          }
+          *reinterpret_cast<float4 *>(po + (t + step * i) * p.o.st + yy) = v;
+        }
+      } else {
+        for (int e = tid; e < m * p.Y; e += blockDim.x) {
+          const int i = e / p.Y, yy = e % p.Y;
+          const float v = so[i * YS + yy];
+          store1<E>(po, (t + step * i) * p.o.st + yy, nx == 2 ? v + so[(kTB + i) * YS + yy] : v);
+        }
+      }
+    }
+    buf ^= VEC ? 1 : 0;
+  }
+  float *dst = !OUT ? p.seg + blockIdx.x * XY : p.nseg == 1 && p.s_out ? p.s_out + bh * XY : nullptr;
+  if (dst) {
+#pragma unroll
+    for (int r = 0; r < 2 * QX; ++r) {
+      float2 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = unpair(S[r][e]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int x = x0 + 16 * (r >> 1) + 2 * (r & 1) + i;
+        if (x >= p.X) continue;
+        float *d = dst + (int64_t)x * p.Y + y0;
+        const float f[4] = {i ? v[0].y : v[0].x, i ? v[1].y : v[1].x, i ? v[2].y : v[2].x, i ? v[3].y : v[3].x};
+        if ((p.Y & 3) == 0 && y0 < p.Y) {
+          *reinterpret_cast<float4 *>(d) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (y0 + e < p.Y) d[e] = f[e];
+        }
+      }
+    }
+  }
+  if (OUT)
+    for (int64_t t = t1; t < tz; ++t)  // padding
+      for (int yy = tid; yy < p.Y; yy += blockDim.x) store1<E>(po, t * p.o.st + yy, 0.f);
+}
+
+// Joins the segments of every head in time order (or reverse): p.seg holds
+// the segments' sums and receives the states at their starts; the state after
+// the last one goes to s_out.  One thread per state element; eight segments'
+// loads are in flight at a time, and the sum goes through them in order.
+__global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__ Group g) {
+  const Pass &p = g.p[blockIdx.y];
+  const int64_t XY = (int64_t)p.X * p.Y;
+  const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (e >= p.B * p.H * XY) return;
+  const int64_t bh = e / XY;
+  const int f = (int)(e % XY);
+  const int64_t n = row_len(p, bh / p.H);
+  const float gd = p.log_decay[bh % p.H];
+  float run = 0.f;
+  if (p.s_in) {
+    const int x = f / p.Y, y = f % p.Y;
+    run = p.s_in[bh * XY + (p.s_in_t ? y * p.X + x : f)];
+  }
+  float *base = p.seg + bh * p.nseg * XY + f;
+  constexpr int kAhead = 8;
+  for (int s0 = 0; s0 < p.nseg; s0 += kAhead) {
+    float v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = p.reverse ? p.nseg - 1 - (s0 + i) : s0 + i;
+      v[i] = s0 + i < p.nseg ? base[s * XY] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (s0 + i < p.nseg) {
+        const int s = p.reverse ? p.nseg - 1 - (s0 + i) : s0 + i;
+        const int64_t len = max((int64_t)0, min(p.seg_len, n - s * p.seg_len));
+        base[s * XY] = run;
+        run = decayed(run, decay_of(gd, len)) + v[i];
+      }
+    }
+  }
+  if (p.s_out) p.s_out[bh * XY + f] = run;
 }
 
 // Sum over the 8 lanes of equal lane % 4 of four columns each: afterwards a
@@ -95,155 +406,14 @@ __device__ __forceinline__ void store_state(const float (&S)[RX][4], float *s, i
   }
 }
 
-// One pass of the recurrence over a segment of a head (blockIdx.x: head and
-// segment, blockIdx.y: 16 columns per warp).  OUT: outputs, from the
-// segment's start state; otherwise the segment's sum alone, from zero.
-template <typename E, int RX, bool OUT>
-__global__ void __launch_bounds__(32 * kRecWarps) rec_kernel(Pass p) {
-  constexpr int XP = 8 * RX;
-  extern __shared__ float rec_smem[];
-  const int nw = blockDim.x >> 5, YB = 16 * nw;
-  float *sb = rec_smem, *sc = sb + kTB * XP, *sa = sc + kTB * YB, *so = sa + kTB * XP;  // sa, so: OUT only
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int x0 = (lane >> 2) * RX, yw = 16 * warp + 4 * (lane & 3), yb = blockIdx.y * YB;
-  const int64_t bh = blockIdx.x / p.nseg, sg = blockIdx.x % p.nseg;
-  const int64_t b = bh / p.H, h = bh % p.H;
-  const int64_t n = row_len(p, b);
-  const int64_t t0 = sg * p.seg_len, tz = min(t0 + p.seg_len, p.T), t1 = max(t0, min(tz, n));
-  const Decay lam = decay_of(p.log_decay[h], 1);
-  const int64_t oa = b * p.a.sb + h * p.a.sh, ob = b * p.b.sb + h * p.b.sh, oc = b * p.c.sb + h * p.c.sh,
-                oo = b * p.o.sb + h * p.o.sh;
-  const int64_t XY = (int64_t)p.X * p.Y;
-
-  float S[RX][4];
-  const float *s0 = !OUT ? nullptr : p.nseg > 1 ? p.seg + blockIdx.x * XY : p.s_in ? p.s_in + bh * XY : nullptr;
-  if (s0) {
-    load_state<RX>(S, s0, p.X, p.Y, x0, yb + yw, p.nseg == 1 && p.s_in_t);
-  } else {
-#pragma unroll
-    for (int r = 0; r < RX; ++r) S[r][0] = S[r][1] = S[r][2] = S[r][3] = 0.f;
-  }
-
-  const int64_t count = t1 - t0;
-  for (int64_t s = 0; s < count; s += kTB) {
-    const int m = (int)min((int64_t)kTB, count - s);
-    // row i of this batch is position t0 + s + i, or t1 - 1 - s - i in reverse
-    const int64_t first = p.reverse ? t1 - 1 - s : t0 + s;
-    const int64_t step = p.reverse ? -1 : 1;
-    __syncthreads();
-    for (int e = threadIdx.x; e < m * XP; e += blockDim.x) {
-      const int i = e / XP, x = e % XP;
-      const int64_t t = first + step * i;
-      sb[e] = x < p.X ? p.sk * load1<E>(p.b.p, ob + t * p.b.st + x) : 0.f;
-      if (OUT) sa[e] = x < p.X ? load1<E>(p.a.p, oa + t * p.a.st + x) : 0.f;
-    }
-    for (int e = threadIdx.x; e < m * YB; e += blockDim.x) {
-      const int i = e / YB, y = yb + e % YB;
-      sc[e] = y < p.Y ? load1<E>(p.c.p, oc + (first + step * i) * p.c.st + y) : 0.f;
-    }
-    __syncthreads();
-    for (int i = 0; i < m; ++i) {
-      // reverse: the state handed in is not decayed before the first position
-      const Decay f = p.reverse && s + i == 0 ? Decay{0.f, true} : lam;
-      const float4 c = *reinterpret_cast<const float4 *>(sc + i * YB + yw);
-      float y[4] = {0.f, 0.f, 0.f, 0.f};
-      auto token = [&](auto decay1) {
-#pragma unroll
-        for (int r4 = 0; r4 < RX; r4 += 4) {
-          const float4 bv = *reinterpret_cast<const float4 *>(sb + i * XP + x0 + r4);
-          float4 av = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (OUT) av = *reinterpret_cast<const float4 *>(sa + i * XP + x0 + r4);
-          const float br[4] = {bv.x, bv.y, bv.z, bv.w}, ar[4] = {av.x, av.y, av.z, av.w}, cr[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float &R = S[r4 + q][e];
-              R = fmaf(br[q], cr[e], decay1(R));
-              if (OUT) y[e] = fmaf(ar[q], R, y[e]);
-            }
-          }
-        }
-      };
-      if (f.near_one)  // one branch per position instead of a select per element
-        token([&](float x) { return fmaf(x, f.m, x); });
-      else
-        token([&](float x) { return x * f.m; });
-      if (OUT) {
-        const float z = reduce_columns(y, lane);
-        if (!(lane & 4)) so[i * YB + 16 * warp + reduced_column(lane)] = p.si * z;
-      }
-    }
-    if (OUT) {
-      __syncthreads();
-      for (int e = threadIdx.x; e < m * YB; e += blockDim.x) {
-        const int i = e / YB, y = yb + e % YB;
-        if (y < p.Y) store1<E>(p.o.p, oo + (first + step * i) * p.o.st + y, so[e]);
-      }
-    }
-  }
-  if (p.reverse && count > 0) {
-#pragma unroll
-    for (int r = 0; r < RX; ++r)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) S[r][q] = decayed(S[r][q], lam);
-  }
-  if (!OUT) {
-    store_state<RX>(S, p.seg + blockIdx.x * XY, p.X, p.Y, x0, yb + yw);
-  } else {
-    if (p.nseg == 1 && p.s_out) store_state<RX>(S, p.s_out + bh * XY, p.X, p.Y, x0, yb + yw);
-    for (int64_t t = t1; t < tz; ++t)  // padding
-      for (int y = yb + threadIdx.x; y < min(p.Y, yb + YB); y += blockDim.x) store1<E>(p.o.p, oo + t * p.o.st + y, 0.f);
-  }
-}
-
-// Joins the segments of every head in time order (or reverse): p.seg holds
-// the segments' sums and receives the states at their starts; the state after
-// the last one goes to s_out.  One thread per state element; eight segments'
-// loads are in flight at a time, and the sum goes through them in order.
-__global__ void __launch_bounds__(256) decay_scan_kernel(Pass p) {
-  const int64_t XY = (int64_t)p.X * p.Y;
-  const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (e >= p.B * p.H * XY) return;
-  const int64_t bh = e / XY;
-  const int f = (int)(e % XY);
-  const int64_t n = row_len(p, bh / p.H);
-  const float g = p.log_decay[bh % p.H];
-  float run = 0.f;
-  if (p.s_in) {
-    const int x = f / p.Y, y = f % p.Y;
-    run = p.s_in[bh * XY + (p.s_in_t ? y * p.X + x : f)];
-  }
-  float *base = p.seg + bh * p.nseg * XY + f;
-  constexpr int kBatch = 8;
-  for (int s0 = 0; s0 < p.nseg; s0 += kBatch) {
-    float v[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int s = p.reverse ? p.nseg - 1 - (s0 + i) : s0 + i;
-      v[i] = s0 + i < p.nseg ? base[s * XY] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (s0 + i < p.nseg) {
-        const int s = p.reverse ? p.nseg - 1 - (s0 + i) : s0 + i;
-        const int64_t len = max((int64_t)0, min(p.seg_len, n - s * p.seg_len));
-        base[s * XY] = run;
-        run = decayed(run, decay_of(g, len)) + v[i];
-      }
-    }
-  }
-  if (p.s_out) p.s_out[bh * XY + f] = run;
-}
-
 // One token: the state read once and written once, 8 N H D M bytes, which is
 // all there is to it (a few FMAs per 8 bytes).  A block is one sequence and
 // head, a warp 16 columns; each lane has its RX float4s of state in flight
 // before anything else.
 template <typename E, int RX>
-__global__ void __launch_bounds__(32 * kRecWarps) decay_step_kernel(StepArgs s) {
+__global__ void __launch_bounds__(32 * kStepWarps) decay_step_kernel(StepArgs s) {
   constexpr int XP = 8 * RX;
-  __shared__ float sq[XP], sk[XP], sv[16 * kRecWarps];
+  __shared__ float sq[XP], sk[XP], sv[16 * kStepWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int x0 = (lane >> 2) * RX, y0 = 16 * warp + 4 * (lane & 3);
   const int64_t nh = blockIdx.x, n = nh / s.H, h = nh % s.H;
@@ -277,19 +447,29 @@ __global__ void __launch_bounds__(32 * kRecWarps) decay_step_kernel(StepArgs s) 
 }
 
 namespace {
-template <typename E, int RX>
-cudaError_t rec_t(const Pass &p, bool sums_only, cudaStream_t st) {
-  const int nw = std::min(kRecWarps, (p.Y + 15) / 16);
-  const dim3 grid((unsigned)(p.B * p.H * p.nseg), (unsigned)((p.Y + 16 * nw - 1) / (16 * nw)));
-  const size_t half = sizeof(float) * kTB * (8 * RX + 16 * nw);
-  return sums_only ? launch_kernel(rec_kernel<E, RX, false>, grid, dim3(32 * nw), half, st, p)
-                   : launch_kernel(rec_kernel<E, RX, true>, grid, dim3(32 * nw), 2 * half, st, p);
+template <typename E, int TX, bool VEC>
+cudaError_t rec_t(const Group &g, int nx, int nwy, bool sums_only, cudaStream_t st) {
+  const Pass &p = g.p[0];
+  const dim3 grid((unsigned)(p.B * p.H * p.nseg), (unsigned)g.n), block(32 * nx * nwy);
+  const size_t rows = sizeof(float) * (VEC ? 2 : 1) * kTB * 4 * TX * nx, cols = sizeof(float) * kTB * 32 * nwy;
+  const size_t smem = sums_only ? rows + (VEC ? 2 : 1) * cols : 2 * rows + (VEC ? 2 : 1) * cols + nx * cols;
+  int blocks = 0;  // raises the kernel's shared-memory limit
+  const void *kern = sums_only ? (const void *)rec_kernel<E, TX, false, VEC> : (const void *)rec_kernel<E, TX, true, VEC>;
+  const cudaError_t e = blocks_per_sm(kern, (int)block.x, (int)smem, &blocks);
+  if (e != cudaSuccess) return e;
+  return sums_only ? launch_kernel(rec_kernel<E, TX, false, VEC>, grid, block, smem, st, g, nx, nwy)
+                   : launch_kernel(rec_kernel<E, TX, true, VEC>, grid, block, smem, st, g, nx, nwy);
 }
-template <typename E>
-cudaError_t rec_e(const Pass &p, bool sums_only, cudaStream_t st) {
-  return p.X <= 32   ? rec_t<E, 4>(p, sums_only, st)
-         : p.X <= 64 ? rec_t<E, 8>(p, sums_only, st)
-                     : rec_t<E, 16>(p, sums_only, st);
+bool pieces16(const View &v, const Pass &p) {
+  auto fits = [](int64_t s, int64_t n) { return n <= 1 || s % 4 == 0; };
+  return ((uintptr_t)v.p & 15u) == 0 && fits(v.sb, p.B) && fits(v.st, p.T) && fits(v.sh, p.H);
+}
+template <typename E, bool VEC>
+cudaError_t rec_v(const Group &g, bool sums_only, cudaStream_t st) {
+  int y = 0;
+  for (int i = 0; i < g.n; ++i) y = std::max(y, g.p[i].Y);
+  const int nwy = (y + 31) / 32, cls = rec_class(g.p[0].X);
+  return cls == 0 ? rec_t<E, 8, VEC>(g, 1, nwy, sums_only, st) : rec_t<E, 16, VEC>(g, cls, nwy, sums_only, st);
 }
 template <typename E>
 cudaError_t step_e(const StepArgs &s, cudaStream_t st) {
@@ -300,12 +480,30 @@ cudaError_t step_e(const StepArgs &s, cudaStream_t st) {
 }
 }  // namespace
 
-cudaError_t launch_rec(const Pass &p, int dtype, bool sums_only, cudaStream_t st) {
-  return dtype == 0 ? rec_e<float>(p, sums_only, st) : rec_e<uint16_t>(p, sums_only, st);
+// Rows in one warp (32 or 64), or two warps of 64.
+int rec_class(int X) { return X <= 32 ? 0 : X <= 64 ? 1 : 2; }
+int64_t rec_segments(int64_t BH, int64_t T, int X, int Y, int npass, int sms) {
+  // The chain of a segment's positions is latency-bound below about two warps
+  // per scheduler, so heads are split until there are that many, down to 64
+  // positions per segment (the sums' pass costs about half of an output pass,
+  // and each segment one state of traffic).
+  const int64_t warps = npass * BH * ((Y + 31) / 32) * (X <= 64 ? 1 : 2), want = 8 * (int64_t)sms;
+  if (warps * 2 >= want) return 1;
+  return std::max<int64_t>(1, std::min((want + warps - 1) / warps, T / 64));
 }
-cudaError_t launch_scan(const Pass &p, cudaStream_t st) {
+cudaError_t launch_rec(const Group &g, int dtype, bool sums_only, cudaStream_t st) {
+  if (dtype != 0) return rec_v<uint16_t, false>(g, sums_only, st);
+  bool vec = true;
+  for (int i = 0; i < g.n; ++i) {
+    const Pass &p = g.p[i];
+    vec = vec && p.X % 4 == 0 && p.Y % 4 == 0 && pieces16(p.a, p) && pieces16(p.b, p) && pieces16(p.c, p) && pieces16(p.o, p);
+  }
+  return vec ? rec_v<float, true>(g, sums_only, st) : rec_v<float, false>(g, sums_only, st);
+}
+cudaError_t launch_scan(const Group &g, cudaStream_t st) {
+  const Pass &p = g.p[0];
   const int64_t n = p.B * p.H * p.X * p.Y;
-  return launch_kernel(decay_scan_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, p);
+  return launch_kernel(decay_scan_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)g.n), dim3(256), 0, st, g);
 }
 cudaError_t launch_step(const StepArgs &s, int dtype, cudaStream_t st) {
   return dtype == 0 ? step_e<float>(s, st) : step_e<uint16_t>(s, st);

@@ -566,11 +566,16 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
   mbar_wait(smem_addr(&s->drain), 0, kBudgetNs, nullptr);
 }
 
+struct Maps {
+  CUtensorMap a[3], b[3], c[3];
+  int terms[3], wide[3];
+};
 template <int XP, int YP, bool OUT>
-__global__ void __launch_bounds__(OUT ? 576 : 320, 1) decay_tc_kernel(const __grid_constant__ CUtensorMap am,
-                                                                      const __grid_constant__ CUtensorMap bm,
-                                                                      const __grid_constant__ CUtensorMap cm, Pass p,
-                                                                      int terms, int wide) {
+__global__ void __launch_bounds__(OUT ? 576 : 320, 1) decay_tc_kernel(const __grid_constant__ Maps maps,
+                                                                      const __grid_constant__ Group group) {
+  const Pass &p = group.p[blockIdx.y];
+  const CUtensorMap &am = maps.a[blockIdx.y], &bm = maps.b[blockIdx.y], &cm = maps.c[blockIdx.y];
+  const int terms = maps.terms[blockIdx.y], wide = maps.wide[blockIdx.y];
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
   uint8_t *sm = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
@@ -674,8 +679,8 @@ bool rows16(const View &v, const Pass &p, bool tma) {
   return ((uintptr_t)v.p & 15u) == 0 && fits(v.sb, p.B) && fits(v.st, p.T) && fits(v.sh, p.H);
 }
 template <int XP, int YP, bool OUT>
-cudaError_t launch_t(const Pass &p, int terms, cudaStream_t st) {
-  CUtensorMap am{}, bm{}, cm{};
+cudaError_t launch_t(const Group &g, cudaStream_t st) {
+  Maps m{};
   if (!encoder() || !ensure_context()) return cudaErrorNotSupported;
   const auto kern = decay_tc_kernel<XP, YP, OUT>;
   constexpr int smem = (int)Tiles<XP, YP>::BYTES + 1024;
@@ -683,18 +688,24 @@ cudaError_t launch_t(const Pass &p, int terms, cudaStream_t st) {
   const cudaError_t e = blocks_per_sm((const void *)kern, OUT ? 576 : 320, smem, &blocks);
   if (e != cudaSuccess) return e;
   if (blocks < 1) return cudaErrorInvalidConfiguration;
-  if ((OUT && !encode(&am, p.a, p, p.X)) || !encode(&bm, p.b, p, p.X) || !encode(&cm, p.c, p, p.Y))
-    return cudaErrorInvalidValue;
   auto even = [](int64_t s, int64_t n) { return n <= 1 || s % 16 == 0; };
-  const int wide = OUT && ((uintptr_t)p.o.p & 31u) == 0 && p.Y % 16 == 0 && even(p.o.sb, p.B) && even(p.o.st, p.T) &&
-                   even(p.o.sh, p.H);
-  return launch_kernel(kern, dim3((unsigned)(p.B * p.H * p.nseg)), dim3(OUT ? 576 : 320), smem, st, am, bm, cm, p,
-                       terms, wide);
+  for (int i = 0; i < g.n; ++i) {
+    const Pass &p = g.p[i];
+    if ((OUT && !encode(&m.a[i], p.a, p, p.X)) || !encode(&m.b[i], p.b, p, p.X) || !encode(&m.c[i], p.c, p, p.Y))
+      return cudaErrorInvalidValue;
+    m.wide[i] = OUT && ((uintptr_t)p.o.p & 31u) == 0 && p.Y % 16 == 0 && even(p.o.sb, p.B) && even(p.o.st, p.T) &&
+                even(p.o.sh, p.H);
+    // states that a call may hand out are float32; those that only meet rows as bfloat16 copies need not be
+    m.terms[i] = p.exact_state && (!OUT || p.nseg == 1) ? 3 : 2;
+  }
+  const Pass &p = g.p[0];
+  return launch_kernel(kern, dim3((unsigned)(p.B * p.H * p.nseg), (unsigned)g.n), dim3(OUT ? 576 : 320), smem, st, m, g);
 }
 template <bool OUT>
-cudaError_t launch_o(const Pass &p, int terms, cudaStream_t st) {
-  if (p.X <= 64) return p.Y <= 64 ? launch_t<64, 64, OUT>(p, terms, st) : launch_t<64, 128, OUT>(p, terms, st);
-  return p.Y <= 64 ? launch_t<128, 64, OUT>(p, terms, st) : launch_t<128, 128, OUT>(p, terms, st);
+cudaError_t launch_o(const Group &g, cudaStream_t st) {
+  const int X = g.p[0].X, Y = g.p[0].Y;
+  if (X <= 64) return Y <= 64 ? launch_t<64, 64, OUT>(g, st) : launch_t<64, 128, OUT>(g, st);
+  return Y <= 64 ? launch_t<128, 64, OUT>(g, st) : launch_t<128, 128, OUT>(g, st);
 }
 }  // namespace
 
@@ -702,7 +713,8 @@ bool tc_fits(const Pass &p) {
   return p.X % 8 == 0 && p.Y % 8 == 0 && p.X <= 128 && p.Y <= 128 && rows16(p.a, p, true) && rows16(p.b, p, true) &&
          rows16(p.c, p, true) && rows16(p.o, p, false);
 }
-int64_t tc_segments(int64_t BH, int64_t T, int sms) {
+int64_t tc_segments(int64_t BH, int64_t T, int npass, int sms) {
+  BH *= npass;
   // in units of one chunk's outputs: a segment costs its chunks and about 2 for
   // starting and ending its CTA; a head in several segments also its sums (b
   // and c are read twice) and the scan
@@ -722,10 +734,8 @@ int64_t tc_segment_len(int64_t T, int64_t nseg) {
   const int64_t nch = (T + kL - 1) / kL;
   return (nch + nseg - 1) / nseg * kL;
 }
-cudaError_t launch_tc(const Pass &p, bool sums_only, cudaStream_t st) {
-  // states that a call may hand out are float32; those that only meet rows as bfloat16 copies need not be
-  const int terms = p.exact_state && (sums_only || p.nseg == 1) ? 3 : 2;
-  return sums_only ? launch_o<false>(p, terms, st) : launch_o<true>(p, terms, st);
+cudaError_t launch_tc(const Group &g, bool sums_only, cudaStream_t st) {
+  return sums_only ? launch_o<false>(g, st) : launch_o<true>(g, st);
 }
 
 }  // namespace decay
