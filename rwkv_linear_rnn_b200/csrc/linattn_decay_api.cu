@@ -104,6 +104,8 @@ cudaError_t run_group(Group &g, const Dims &d, bool tc, void *ws, cudaStream_t s
   for (int i = 0; i < g.n; ++i) {
     Pass &p = g.p[i];
     p.nseg = (int)nseg;
+    // the recurrence's last segment has the state itself; the tensor cores' only to the bits its outputs need
+    p.scan_out = tc && nseg > 1 && p.s_out;
     p.seg_len = tc ? tc_segment_len(d.T, nseg) : (d.T + nseg - 1) / nseg;
     p.seg = static_cast<float *>(ws) + i * (seg_bytes(d, nseg) / sizeof(float));
   }

@@ -21,6 +21,7 @@
 // positions at a time (12 shuffles, one float4 stored), over the two warps of
 // a column's rows when they are written out.
 #include <algorithm>
+#include <type_traits>
 
 #include "linattn_decay.cuh"
 
@@ -84,17 +85,33 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool r
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 
+template <int V>
+__device__ __forceinline__ void ldv(float (&x)[V], const float *p) {
+  if constexpr (V == 4) {
+    const float4 f = *reinterpret_cast<const float4 *>(p);
+    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+  } else {
+    x[0] = *p;
+  }
+}
+template <int V>
+__device__ __forceinline__ void stv(float *p, const float (&x)[V]) {
+  if constexpr (V == 4) *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  else *p = x[0];
+}
+
 // Batches of 8 positions are taken relative to their start unless lam^8 is
 // below 2^-16.
 constexpr int kBatch = 8;
 constexpr float kSlowest = -16.f * 0.69314718f / kBatch;
 
 // One pass of the recurrence over a segment of a head (blockIdx.x: head and
-// segment, blockIdx.y: pass).  OUT: outputs, from the segment's start state;
-// otherwise the segment's sum alone, from zero.  VEC: float32 in 16-byte
-// pieces, fetched one batch ahead.
+// segment, blockIdx.y: pass, blockIdx.z: 32 nwy columns).  OUT: outputs, from
+// the segment's start state; otherwise the segment's sum alone, from zero.
+// VEC: float32 in 16-byte pieces, fetched one batch ahead.  168 registers let
+// three warps share a scheduler.
 template <typename E, int TX, bool OUT, bool VEC>
-__global__ void __launch_bounds__(256) rec_kernel(const __grid_constant__ Group g, int nx, int nwy) {
+__global__ void __maxnreg__(168) rec_kernel(const __grid_constant__ Group g, int nx, int nwy) {
   const Pass &p = g.p[blockIdx.y];
   extern __shared__ __align__(16) float rec_smem[];
   constexpr int QX = TX / 4;  // a lane's float4s of rows, 16 rows apart
@@ -102,10 +119,13 @@ __global__ void __launch_bounds__(256) rec_kernel(const __grid_constant__ Group 
   constexpr int NBUF = VEC ? 2 : 1;
   float *sb = rec_smem, *sc = sb + NBUF * kTB * XS, *sa = sc + NBUF * kTB * YS;  // sa, so: OUT only
   float *so = sa + NBUF * kTB * XS;                                           // [nx][kTB][YS]
-  __shared__ float wk[kBatch], uk[kBatch];
+  __shared__ __align__(16) float wk[kBatch], uk[kBatch];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wx = warp % nx;
-  const int rg = lane >> 3, x0 = 4 * TX * wx + 4 * rg, y0 = 32 * (warp / nx) + 4 * (lane & 7);
+  const int rg = lane >> 3, x0 = 4 * TX * wx + 4 * rg, yl = 32 * (warp / nx) + 4 * (lane & 7);
+  const int yt = blockIdx.z * YS, y0 = yt + yl;  // the block's first column, this lane's
   const int64_t bh = blockIdx.x / p.nseg, sg = blockIdx.x % p.nseg;
+  const bool last = sg == (p.reverse ? 0 : p.nseg - 1);  // of the pass's segments
+  if (!OUT && last && !p.scan_out) return;               // no state starts from its sum
   const int64_t b = bh / p.H, h = bh % p.H;
   const int64_t n = row_len(p, b);
   const int64_t t0 = sg * p.seg_len, tz = min(t0 + p.seg_len, p.T), t1 = max(t0, min(tz, n));
@@ -163,23 +183,26 @@ __global__ void __launch_bounds__(256) rec_kernel(const __grid_constant__ Group 
   };
   const Decay lam = decay_of(gd, 1), lam_batch = decay_of(gd, kBatch);
 
-  // rows s.. of the segment (m of them) into buffer `buf`
+  // rows s.. of the segment (m of them) into buffer `buf`.  A thread's pieces
+  // of a and b are one column's, every rx-th row; of c every ry-th.
+  const int ux = XS / 4, uy = YS / 4, rx = blockDim.x / ux, ry = blockDim.x / uy;
+  const int ix = tid / ux, px = 4 * (tid % ux), iy = tid / uy, py = 4 * (tid % uy);
   auto fetch = [&](int64_t s, int m, int buf) {
     float *db = sb + buf * kTB * XS, *dc = sc + buf * kTB * YS, *da = sa + buf * kTB * XS;
     const int64_t t = t_first + step * s;
     if constexpr (VEC) {
-      const int ux = XS / 4, uy = YS / 4;
-      for (int e = tid; e < m * ux; e += blockDim.x) {
-        const int i = e / ux, x = 4 * (e % ux);
-        const bool real = x < p.X;
-        cp_async16(smem_addr(db + 4 * e), pb + (t + step * i) * p.b.st + (real ? x : 0), real);
-        if (OUT) cp_async16(smem_addr(da + 4 * e), pa + (t + step * i) * p.a.st + (real ? x : 0), real);
+      const bool xr = px < p.X, yr = yt + py < p.Y;
+      const E *fb = pb + (t + step * ix) * p.b.st + (xr ? px : 0), *fa = OUT ? pa + (t + step * ix) * p.a.st + (xr ? px : 0) : nullptr;
+      const int64_t jb = step * rx * p.b.st, ja = step * rx * p.a.st;
+      uint32_t ub = smem_addr(db + 4 * tid), ua = smem_addr(da + 4 * tid);
+      for (int i = ix; i < m; i += rx, fb += jb, ub += 16 * blockDim.x) {
+        cp_async16(ub, fb, xr);
+        if (OUT) cp_async16(ua, fa, xr), fa += ja, ua += 16 * blockDim.x;
       }
-      for (int e = tid; e < m * uy; e += blockDim.x) {
-        const int i = e / uy, y = 4 * (e % uy);
-        const bool real = y < p.Y;
-        cp_async16(smem_addr(dc + 4 * e), pc + (t + step * i) * p.c.st + (real ? y : 0), real);
-      }
+      const E *fc = pc + (t + step * iy) * p.c.st + (yr ? yt + py : 0);
+      const int64_t jc = step * ry * p.c.st;
+      uint32_t uc = smem_addr(dc + 4 * tid);
+      for (int i = iy; i < m; i += ry, fc += jc, uc += 16 * blockDim.x) cp_async16(uc, fc, yr);
     } else {
       for (int e = tid; e < m * XS; e += blockDim.x) {
         const int i = e / XS, x = e % XS;
@@ -187,7 +210,7 @@ __global__ void __launch_bounds__(256) rec_kernel(const __grid_constant__ Group 
         if (OUT) da[e] = x < p.X ? load1<E>(pa, (t + step * i) * p.a.st + x) : 0.f;
       }
       for (int e = tid; e < m * YS; e += blockDim.x) {
-        const int i = e / YS, y = e % YS;
+        const int i = e / YS, y = yt + e % YS;
         dc[e] = y < p.Y ? load1<E>(pc, (t + step * i) * p.c.st + y) : 0.f;
       }
     }
@@ -208,20 +231,22 @@ __global__ void __launch_bounds__(256) rec_kernel(const __grid_constant__ Group 
       fetch(s, m, 0);
     }
     __syncthreads();
-    const float *cb = sb + buf * kTB * XS + x0, *cc = sc + buf * kTB * YS + y0, *ca = sa + buf * kTB * XS + x0;
-#pragma unroll 1
-    for (int i0 = 0; i0 < m; i0 += 4) {
+    const float *cb = sb + buf * kTB * XS + x0, *cc = sc + buf * kTB * YS + yl, *ca = sa + buf * kTB * XS + x0;
+    // Four positions from i0; PLAIN: all of them there, and no decay between them.
+    auto four = [&](int i0, auto plain) {
+      constexpr bool PLAIN = decltype(plain)::value;
       f2 y[4][4];
+      const float4 w4 = *reinterpret_cast<const float4 *>(wk + (i0 & (kBatch - 1)));
+      const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[k][e] = 0ull;
         const int i = i0 + k;
-        if (i >= m) continue;
-        if (slow && !p.reverse) decay(lam);
-        const float w = wk[i & (kBatch - 1)];
+        if (!PLAIN && i >= m) continue;
+        if (!PLAIN && slow && !p.reverse) decay(lam);
         const float4 cv = *reinterpret_cast<const float4 *>(cc + i * YS);
-        const f2 c[4] = {both(cv.x * w), both(cv.y * w), both(cv.z * w), both(cv.w * w)};
+        const f2 c[4] = {both(cv.x * w[k]), both(cv.y * w[k]), both(cv.z * w[k]), both(cv.w * w[k])};
 #pragma unroll
         for (int q = 0; q < QX; ++q) {
           const ulonglong2 bv = *reinterpret_cast<const ulonglong2 *>(cb + i * XS + 16 * q);
@@ -239,7 +264,7 @@ __global__ void __launch_bounds__(256) rec_kernel(const __grid_constant__ Group 
             }
           }
         }
-        if (slow && p.reverse) decay(lam);
+        if (!PLAIN && slow && p.reverse) decay(lam);
       }
       if (OUT) {
         // 16 sums over the lanes rg = 0..3: lane rg ends with those of position i0 + rg
@@ -254,42 +279,48 @@ __global__ void __launch_bounds__(256) rec_kernel(const __grid_constant__ Group 
         for (int e = 0; e < 4; ++e)
           o[e] = (rg & 1 ? z[4 + e] : z[e]) + __shfl_xor_sync(~0u, rg & 1 ? z[e] : z[4 + e], 8);
         const float u = uk[(i0 + rg) & (kBatch - 1)];
-        *reinterpret_cast<float4 *>(so + (wx * kTB + i0 + rg) * YS + y0) = make_float4(u * o[0], u * o[1], u * o[2], u * o[3]);
+        *reinterpret_cast<float4 *>(so + (wx * kTB + i0 + rg) * YS + yl) = make_float4(u * o[0], u * o[1], u * o[2], u * o[3]);
       }
-      if (!slow) {
-        if (i0 + 4 >= m) {
-          const int k = m & (kBatch - 1);
-          decay(k == 0 ? lam_batch : decay_of(gd, k));
-        } else if ((i0 & (kBatch - 1)) == kBatch - 4) {
-          decay(lam_batch);
-        }
+    };
+    if (slow) {
+#pragma unroll 1
+      for (int i0 = 0; i0 < m; i0 += 4) four(i0, std::false_type());
+    } else {
+      const int full = m & ~3;
+#pragma unroll 1
+      for (int i0 = 0; i0 < full; i0 += 4) {
+        four(i0, std::true_type());
+        if (i0 & 4) decay(lam_batch);
       }
+      if (full < m) four(full, std::false_type());
+      if (m & (kBatch - 1)) decay(decay_of(gd, m & (kBatch - 1)));
     }
     __syncthreads();
     if (OUT) {
       const int64_t t = t_first + step * s;
       if constexpr (VEC) {
-        const int uy = p.Y / 4;
-        for (int e = tid; e < m * uy; e += blockDim.x) {
-          const int i = e / uy, yy = 4 * (e % uy);
-          float4 v = *reinterpret_cast<const float4 *>(so + i * YS + yy);
-          if (nx == 2) {
-            const float4 u = *reinterpret_cast<const float4 *>(so + (kTB + i) * YS + yy);
-            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        float *fo = po + (t + step * iy) * p.o.st + yt + py;
+        const int64_t jo = step * ry * p.o.st;
+        const float *uo = so + 4 * tid;
+        if (yt + py < p.Y)
+          for (int i = iy; i < m; i += ry, fo += jo, uo += 4 * blockDim.x) {
+            float4 v = *reinterpret_cast<const float4 *>(uo);
+            if (nx == 2) {
+              const float4 u = *reinterpret_cast<const float4 *>(uo + kTB * YS);
+              v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+            }
+            *reinterpret_cast<float4 *>(fo) = v;
           }
-          *reinterpret_cast<float4 *>(po + (t + step * i) * p.o.st + yy) = v;
-        }
       } else {
-        for (int e = tid; e < m * p.Y; e += blockDim.x) {
-          const int i = e / p.Y, yy = e % p.Y;
-          const float v = so[i * YS + yy];
-          store1<E>(po, (t + step * i) * p.o.st + yy, nx == 2 ? v + so[(kTB + i) * YS + yy] : v);
+        for (int e = tid; e < m * YS; e += blockDim.x) {
+          const int i = e / YS, y = yt + e % YS;
+          if (y < p.Y) store1<E>(po, (t + step * i) * p.o.st + y, nx == 2 ? so[e] + so[kTB * YS + e] : so[e]);
         }
       }
     }
     buf ^= VEC ? 1 : 0;
   }
-  float *dst = !OUT ? p.seg + blockIdx.x * XY : p.nseg == 1 && p.s_out ? p.s_out + bh * XY : nullptr;
+  float *dst = !OUT ? p.seg + blockIdx.x * XY : last && p.s_out && !p.scan_out ? p.s_out + bh * XY : nullptr;
   if (dst) {
 #pragma unroll
     for (int r = 0; r < 2 * QX; ++r) {
@@ -314,47 +345,56 @@ __global__ void __launch_bounds__(256) rec_kernel(const __grid_constant__ Group 
   }
   if (OUT)
     for (int64_t t = t1; t < tz; ++t)  // padding
-      for (int yy = tid; yy < p.Y; yy += blockDim.x) store1<E>(po, t * p.o.st + yy, 0.f);
+      for (int y = yt + tid; y < min(p.Y, yt + YS); y += blockDim.x) store1<E>(po, t * p.o.st + y, 0.f);
 }
 
 // Joins the segments of every head in time order (or reverse): p.seg holds
 // the segments' sums and receives the states at their starts; the state after
-// the last one goes to s_out.  One thread per state element; eight segments'
-// loads are in flight at a time, and the sum goes through them in order.
+// the last one goes to s_out if the pass leaves it to this kernel.  blockIdx.y
+// is the head, blockIdx.z the pass; V state elements per thread.  Eight
+// segments' loads are in flight at a time, and the sum goes through them in
+// order.
+template <int V>
 __global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__ Group g) {
-  const Pass &p = g.p[blockIdx.y];
-  const int64_t XY = (int64_t)p.X * p.Y;
-  const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (e >= p.B * p.H * XY) return;
-  const int64_t bh = e / XY;
-  const int f = (int)(e % XY);
+  const Pass &p = g.p[blockIdx.z];
+  const int XY = p.X * p.Y, f = ((int)blockIdx.x * 256 + (int)threadIdx.x) * V;
+  if (f >= XY) return;
+  const int64_t bh = blockIdx.y;
   const int64_t n = row_len(p, bh / p.H);
   const float gd = p.log_decay[bh % p.H];
-  float run = 0.f;
+  const Decay whole = decay_of(gd, p.seg_len);
+  float run[V] = {};
   if (p.s_in) {
-    const int x = f / p.Y, y = f % p.Y;
-    run = p.s_in[bh * XY + (p.s_in_t ? y * p.X + x : f)];
+    const float *s = p.s_in + bh * XY;
+    if (!p.s_in_t) ldv(run, s + f);
+    else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) run[i] = s[(f + i) % p.Y * p.X + (f + i) / p.Y];
+    }
   }
   float *base = p.seg + bh * p.nseg * XY + f;
   constexpr int kAhead = 8;
+  const int use = p.nseg - (p.scan_out ? 0 : 1);  // sums that somebody starts from
   for (int s0 = 0; s0 < p.nseg; s0 += kAhead) {
-    float v[kAhead];
+    float v[kAhead][V] = {};
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int s = p.reverse ? p.nseg - 1 - (s0 + i) : s0 + i;
-      v[i] = s0 + i < p.nseg ? base[s * XY] : 0.f;
+      if (s0 + i < use) ldv(v[i], base + (int64_t)s * XY);
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (s0 + i < p.nseg) {
         const int s = p.reverse ? p.nseg - 1 - (s0 + i) : s0 + i;
         const int64_t len = max((int64_t)0, min(p.seg_len, n - s * p.seg_len));
-        base[s * XY] = run;
-        run = decayed(run, decay_of(gd, len)) + v[i];
+        stv(base + (int64_t)s * XY, run);
+        const Decay d = len == p.seg_len ? whole : decay_of(gd, len);
+#pragma unroll
+        for (int e = 0; e < V; ++e) run[e] = decayed(run[e], d) + v[i][e];
       }
     }
   }
-  if (p.s_out) p.s_out[bh * XY + f] = run;
+  if (p.s_out && p.scan_out) stv(p.s_out + bh * XY + f, run);
 }
 
 // Sum over the 8 lanes of equal lane % 4 of four columns each: afterwards a
@@ -447,10 +487,13 @@ __global__ void __launch_bounds__(32 * kStepWarps) decay_step_kernel(StepArgs s)
 }
 
 namespace {
+// Warps of 32 columns in a block; 128 columns are two blocks of two, so that
+// 12 warps fit an SM with two warps of rows as well.
+int rec_warps_y(int Y) { return Y > 96 ? 2 : (Y + 31) / 32; }
 template <typename E, int TX, bool VEC>
-cudaError_t rec_t(const Group &g, int nx, int nwy, bool sums_only, cudaStream_t st) {
+cudaError_t rec_t(const Group &g, int nx, int nwy, int ytiles, bool sums_only, cudaStream_t st) {
   const Pass &p = g.p[0];
-  const dim3 grid((unsigned)(p.B * p.H * p.nseg), (unsigned)g.n), block(32 * nx * nwy);
+  const dim3 grid((unsigned)(p.B * p.H * p.nseg), (unsigned)g.n, (unsigned)ytiles), block(32 * nx * nwy);
   const size_t rows = sizeof(float) * (VEC ? 2 : 1) * kTB * 4 * TX * nx, cols = sizeof(float) * kTB * 32 * nwy;
   const size_t smem = sums_only ? rows + (VEC ? 2 : 1) * cols : 2 * rows + (VEC ? 2 : 1) * cols + nx * cols;
   int blocks = 0;  // raises the kernel's shared-memory limit
@@ -468,8 +511,8 @@ template <typename E, bool VEC>
 cudaError_t rec_v(const Group &g, bool sums_only, cudaStream_t st) {
   int y = 0;
   for (int i = 0; i < g.n; ++i) y = std::max(y, g.p[i].Y);
-  const int nwy = (y + 31) / 32, cls = rec_class(g.p[0].X);
-  return cls == 0 ? rec_t<E, 8, VEC>(g, 1, nwy, sums_only, st) : rec_t<E, 16, VEC>(g, cls, nwy, sums_only, st);
+  const int nwy = rec_warps_y(y), tiles = (y + 32 * nwy - 1) / (32 * nwy), cls = rec_class(g.p[0].X);
+  return cls == 0 ? rec_t<E, 8, VEC>(g, 1, nwy, tiles, sums_only, st) : rec_t<E, 16, VEC>(g, cls, nwy, tiles, sums_only, st);
 }
 template <typename E>
 cudaError_t step_e(const StepArgs &s, cudaStream_t st) {
@@ -483,13 +526,24 @@ cudaError_t step_e(const StepArgs &s, cudaStream_t st) {
 // Rows in one warp (32 or 64), or two warps of 64.
 int rec_class(int X) { return X <= 32 ? 0 : X <= 64 ? 1 : 2; }
 int64_t rec_segments(int64_t BH, int64_t T, int X, int Y, int npass, int sms) {
-  // The chain of a segment's positions is latency-bound below about two warps
-  // per scheduler, so heads are split until there are that many, down to 64
-  // positions per segment (the sums' pass costs about half of an output pass,
-  // and each segment one state of traffic).
-  const int64_t warps = npass * BH * ((Y + 31) / 32) * (X <= 64 ? 1 : 2), want = 8 * (int64_t)sms;
-  if (warps * 2 >= want) return 1;
-  return std::max<int64_t>(1, std::min((want + warps - 1) / warps, T / 64));
+  // In cycles: a position takes a warp of 64 rows about 150 of its scheduler's,
+  // and at least 300 from one to the next; 12 warps fit an SM at a time.  A
+  // head in several segments costs its sums (half of that again), the scan and
+  // a launch more.
+  const int64_t warps = npass * BH * ((Y + 31) / 32) * (X <= 64 ? 1 : 2);
+  const double each = X <= 32 ? 75. : 150., chain = X <= 32 ? 200. : 300.;
+  int64_t best = 1;
+  double least = 1e300;
+  for (int64_t n = 1; n <= std::max<int64_t>(1, std::min<int64_t>(T / 32, 12 * sms)); ++n) {
+    const int64_t len = (T + n - 1) / n, per_sm = (warps * n + sms - 1) / sms;
+    if (n > 1 && (T + len - 1) / len != n) continue;
+    const double full = (double)(per_sm / 12), rest = (double)((per_sm % 12 + 3) / 4);
+    const double pos = full * std::max(chain, 3 * each) + (rest > 0 ? std::max(chain, rest * each) : 0.);
+    const double t = (n > 1 ? 1.5 : 1.) * pos * (double)len + (n > 1 ? 15000. + 400. * (double)n : 0.);
+    if (t < least) least = t, best = n;
+    if (per_sm > 48) break;
+  }
+  return best;
 }
 cudaError_t launch_rec(const Group &g, int dtype, bool sums_only, cudaStream_t st) {
   if (dtype != 0) return rec_v<uint16_t, false>(g, sums_only, st);
@@ -502,8 +556,10 @@ cudaError_t launch_rec(const Group &g, int dtype, bool sums_only, cudaStream_t s
 }
 cudaError_t launch_scan(const Group &g, cudaStream_t st) {
   const Pass &p = g.p[0];
-  const int64_t n = p.B * p.H * p.X * p.Y;
-  return launch_kernel(decay_scan_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)g.n), dim3(256), 0, st, g);
+  const int n = p.X * p.Y, v = n % 4 == 0 ? 4 : 1;
+  const dim3 grid((unsigned)((n / v + 255) / 256), (unsigned)(p.B * p.H), (unsigned)g.n);
+  return v == 4 ? launch_kernel(decay_scan_kernel<4>, grid, dim3(256), 0, st, g)
+                : launch_kernel(decay_scan_kernel<1>, grid, dim3(256), 0, st, g);
 }
 cudaError_t launch_step(const StepArgs &s, int dtype, cudaStream_t st) {
   return dtype == 0 ? step_e<float>(s, st) : step_e<uint16_t>(s, st);

@@ -576,6 +576,7 @@ __global__ void __launch_bounds__(OUT ? 576 : 320, 1) decay_tc_kernel(const __gr
   const Pass &p = group.p[blockIdx.y];
   const CUtensorMap &am = maps.a[blockIdx.y], &bm = maps.b[blockIdx.y], &cm = maps.c[blockIdx.y];
   const int terms = maps.terms[blockIdx.y], wide = maps.wide[blockIdx.y];
+  if (!OUT && !p.scan_out && (int)blockIdx.x % p.nseg == (p.reverse ? 0 : p.nseg - 1)) return;  // no state starts from it
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
   uint8_t *sm = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
