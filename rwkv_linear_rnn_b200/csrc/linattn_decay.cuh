@@ -87,6 +87,34 @@ __device__ __forceinline__ Decay decay_of(float g, int64_t n) {
 }
 __device__ __forceinline__ float decayed(float x, Decay d) { return fmaf(x, d.m, d.near_one ? x : 0.f); }
 
+// ------------------------------------------------------ two-wide float32 ---
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 both(float x) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(x));
+  return d;
+}
+__device__ __forceinline__ f2 pair(float x, float y) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(f2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+
 // Launches.  Each returns the first launch's failure.  X of one rec_class may
 // share a launch; rec_segments are the segments per head for `npass` passes.
 int rec_class(int X);

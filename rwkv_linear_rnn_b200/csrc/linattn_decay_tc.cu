@@ -15,20 +15,26 @@
 // 128 x Y x 128, 128 x Y x X, and X x Y x 128 for the state, which stays in
 // tensor memory for the whole segment.
 //
-// Roundings.  P and the copy of R that meets a are rounded to bfloat16 once
-// (they are matrix operands); both errors are independent of the result's own
-// rounding and as large.  Weights lam^n are never multiplied into a bfloat16
-// operand with a single rounding: the scores are weighted in float32 before
-// the rounding of P, the product with R is weighted in float32 afterwards, and
-// the weighted keys enter the state as a sum of three bfloat16 terms (24 bits)
-// in the passes that can hand it out (asked to or not, so that the outputs are
-// the same bits), or two (16 bits, below the rounding of R's copy) elsewhere.
+// Roundings.  P, the copy of R that meets a and, in passes that cannot hand
+// their state out, the weighted keys lam^n b are rounded to bfloat16 once (they
+// are matrix operands); these errors are independent of the result's own
+// rounding and as large.  Weights are applied in float32 before the rounding
+// (P, keys) or afterwards (a R).  In passes that can hand their state out
+// (asked to or not, so that the outputs are the same bits) the weighted keys
+// are a sum of two bfloat16 terms, 17 bits with the second's sign (a state's
+// error is then about 2e-6 of it, half a bit of each sum of 128 products).
 //
 // One CTA runs one head's segment with specialised warps: a producer (TMA
-// loads), an MMA issuer, two warpgroups for the state (weighted keys; state
-// copy and decay), one for P, one for the outputs.  The floor is HBM: a chunk
-// of 128 x (X + X + Y + Y) bfloat16 takes 2.9 us of an SM's share of the
-// measured bandwidth at X = Y = 128 against about 1.7 us of MMAs.
+// loads), an MMA issuer, a warpgroup for the state (its bfloat16 copy and its
+// decay), one for the outputs, two for P and the weighted keys.  The MMAs of a
+// chunk are issued in the order scores, keys (first term), a R, keys (other
+// terms), P c, so that each step of a warpgroup has the products of others to
+// hide behind: P behind keys and a R, the state's step behind P c and the next
+// scores, the next chunk's keys behind all of them.
+//
+// The floor is HBM: a chunk of 128 x (X + X + Y + Y) bfloat16 takes 2.9 us of
+// an SM's share of the measured bandwidth at X = Y = 128; its MMAs take 1.1 us
+// (1.4 with two terms).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -44,7 +50,7 @@ namespace decay {
 constexpr int kL = 128;                  // positions per chunk
 constexpr uint32_t kHalf = kL * 128;     // bytes of 128 rows of 64 bfloat16
 constexpr uint32_t kTmemCols = 512;
-constexpr int64_t kBudgetNs = 1000000000;  // bound on any one wait
+constexpr uint32_t kTries = 1u << 23;    // bound on any one wait
 
 // ------------------------------------------------------------ tcgen05 ---
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t ncols) {
@@ -71,6 +77,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
 }
+// One lane of a converged warp.  The MMA and load warps run their loops whole
+// and issue under this election: with operands that the compiler knows to be
+// the same in every lane a tcgen05.mma is one instruction (in a branch on the
+// lane's index each costs about 130 cycles).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
+}
 // Arrive on `bar` once every MMA issued so far by this thread is complete.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -86,11 +101,20 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[3
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // Uses of r stay behind the wait that stands before this.
-__device__ __forceinline__ void pin(uint32_t (&r)[32]) {
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N]) {
 #pragma unroll
-  for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k]));
+  for (int k = 0; k < N; ++k) asm volatile("" : "+r"(r[k]));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -103,13 +127,10 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // Shared-memory matrix descriptors of tiles in the 128-byte swizzle: rows of
@@ -118,15 +139,15 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t 
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
-// Contraction along the rows' 64-wide halves (128 rows), 16-wide step k16.
-__device__ __forceinline__ uint64_t kmajor(uint32_t tile, int k16) {
-  return sdesc(tile + kHalf * (k16 >> 2) + 32u * (k16 & 3), 16u, 1024u);
-}
+// Contraction along the rows' 64-wide halves (128 rows); the step to the
+// 16-wide slice k16 (addresses below 256 KB do not carry out of their field).
+__device__ __forceinline__ uint64_t kmajor(uint32_t tile) { return sdesc(tile, 16u, 1024u); }
+__device__ __forceinline__ constexpr uint32_t kstep(int k16) { return (kHalf * (k16 >> 2) + 32u * (k16 & 3)) >> 4; }
 // Contraction down the rows; `half` bytes between 64-wide groups of columns.
-__device__ __forceinline__ uint64_t mnmajor(uint32_t tile, int k16, uint32_t half) {
-  return sdesc(tile + 2048u * k16, half, 1024u);
-}
-// Instruction descriptor: bf16 x bf16 -> f32, M x N, operand majors.
+__device__ __forceinline__ uint64_t mnmajor(uint32_t tile, uint32_t half) { return sdesc(tile, half, 1024u); }
+__device__ __forceinline__ constexpr uint32_t mnstep(int k16) { return 2048u * k16 >> 4; }
+// Instruction descriptor: bf16 x bf16 -> f32, M x N, operand majors, A negated.
+constexpr uint32_t kNegateA = 1u << 13;
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -149,57 +170,97 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// Pairs of bfloat16, each operation rounded once.
+__device__ __forceinline__ uint32_t mulb(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t fmab(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(f2 v) {
+  const float2 f = unpair(v);
+  return pack2(f.x, f.y);
+}
+__device__ __forceinline__ f2 pair_at(const uint32_t *r) { return pair(__uint_as_float(r[0]), __uint_as_float(r[1])); }
 // lam^n for n >= 0 (1 for n = 0 whatever lam is); g2 = log_decay log2(e).
 __device__ __forceinline__ float power(float g2, int64_t n) { return n == 0 ? 1.f : ex2(g2 * (float)n); }
 
 // ------------------------------------------------------------- the pass ---
-// Shared memory: NB stages of b, one tile for the weighted keys' second term
-// (their first and third take the place of b), NC stages of c, NA of a, and
-// the state's bfloat16 copy.  With X = 64 the state's products run with
-// M = 128: their rows from 64 on are the bytes of the tile behind b's (there
-// always is one) and their results are not read.
-template <int XP, int YP>
+// Shared memory: two buffers for the terms of the weighted keys, a ring of NS
+// tiles that the chunks' a, b and c pass through in this order, and the
+// state's bfloat16 copy.  With four slots each tile's load is issued half a
+// chunk's time or more before its first use.  With X = 64 the state's products run with
+// M = 128: their rows from 64 on are the bytes behind the term (there always
+// are some) and their results are not read.
+template <int XP, int YP, bool OUT>
 struct Tiles {
-  static constexpr uint32_t BT = XP / 64 * kHalf, CT = YP / 64 * kHalf, RT = YP / 64 * XP * 128;
-  static constexpr int NB = XP == 128 ? 2 : YP == 128 ? 3 : 4;
-  static constexpr int NA = XP == 128 ? (YP == 128 ? 1 : 2) : 3;
-  static constexpr int NC = YP == 128 ? (XP == 128 ? 2 : 3) : XP == 128 ? 3 : 4;
-  static constexpr uint32_t B = 0, W2 = B + NB * BT, C = W2 + BT, A = C + NC * CT, R = A + NA * BT, BYTES = R + RT;
+  static constexpr uint32_t BT = XP / 64 * kHalf, CT = YP / 64 * kHalf, RT = OUT ? YP / 64 * XP * 128 : 0;
+  static constexpr uint32_t SLOT = BT > CT ? BT : CT;
+  static constexpr uint32_t MOST = 224 * 1024;
+  static constexpr int NS = (int)((MOST - 2 * BT - RT) / SLOT) < 8 ? (int)((MOST - 2 * BT - RT) / SLOT) : 8;
+  static constexpr int PER = OUT ? 3 : 2;  // tiles of a chunk: (a,) b, c
+  static constexpr uint32_t W = 0, RING = 2 * BT, R = RING + NS * SLOT, BYTES = R + RT;
+  static_assert(NS >= 4 && BYTES <= MOST, "the tiles, their alignment and the barriers fit 227 KB");
 };
-static_assert(Tiles<128, 128>::BYTES == 224 * 1024 && Tiles<64, 128>::BYTES == 224 * 1024 &&
-                  Tiles<128, 64>::BYTES == 224 * 1024 && Tiles<64, 64>::BYTES <= 224 * 1024,
-              "the tiles, their alignment and the barriers fit 227 KB");
 
 struct Bars {
-  uint64_t b_full[4], c_full[4], a_full[4], b_empty[4], c_empty[4], a_empty[4];
-  uint64_t scores;    // a b^T complete (MMA)
-  uint64_t p_ready;   // P in tensor memory (P warpgroup)
-  uint64_t w_ready;   // first two terms of the weighted keys in place, c's padding zeroed (state warpgroups)
-  uint64_t w1_done;   // products with the first term complete: the third may overwrite it (MMA)
-  uint64_t w3_ready;  // third term in place (state warpgroups)
-  uint64_t state;     // all products into the state complete (MMA)
-  uint64_t r_ready;   // the state's copy in shared memory, the state decayed in tensor memory (state warpgroups)
-  uint64_t o_done;    // outputs complete in tensor memory (MMA)
-  uint64_t o_free;    // outputs read (output warpgroup)
-  uint64_t drain;     // every MMA complete
+  uint64_t full[8], empty[8];  // ring slots
+  uint64_t scores;             // a b^T complete (MMA)
+  uint64_t p_ready;            // P in tensor memory (P warpgroups)
+  uint64_t w_full[2];          // a term of the weighted keys in its buffer (key warpgroups)
+  uint64_t w_free[2];          // its products complete (MMA)
+  uint64_t c_clean;            // c's rows behind the last position zeroed (key warpgroups; a segment has one such chunk)
+  uint64_t state;              // a R and all products into the state complete (MMA)
+  uint64_t r_ready;            // the state's copy in shared memory, the state decayed in tensor memory (state warpgroup)
+  uint64_t o_done;             // outputs complete in tensor memory (MMA)
+  uint64_t o_free;             // outputs read (output warpgroup)
+  uint64_t drain;              // every MMA complete
   uint32_t tmem;
-  volatile int fail;  // some wait gave up
   alignas(16) float up[32];  // lam^r, lam^{31-r}; read four at a time
   alignas(16) float down[32];
 };
-constexpr int kStateThreads = 256;
+constexpr int kKeyThreads = 256;
+// Warps of a CTA: 4 state, (4 outputs,) 8 P and keys, loads, MMAs.  Their hot
+// loops are kept short: one that does not fit the instruction cache with the
+// others waits for its instructions, chunk after chunk.
+template <bool OUT>
+struct Roles {
+  static constexpr int KEYS = OUT ? 8 : 4, LOAD = KEYS + 8, MMA = LOAD + 1, THREADS = 32 * (MMA + 1);
+};
 
-// Bounded wait; a wait that gives up stores WKV_ERR_TIMEOUT and ends the CTA.
-__device__ __forceinline__ bool wait(uint64_t &bar, uint32_t parity, Bars *s, int32_t *status) {
-  const uint32_t addr = smem_addr(&bar);
-  if (mbar_try_wait(addr, parity)) return true;
-  if (mbar_wait(addr, parity, kBudgetNs, &s->fail)) return true;
-  s->fail = 1;
-  if (status) atomicCAS(status, 0, -5 /* WKV_ERR_TIMEOUT */);
-  return false;
+// Waits for the phase of `addr` with the given parity, in at most kTries tries
+// (each is suspended by the hardware for a while).
+__device__ __forceinline__ bool spin(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "TRY%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE%=;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra TRY%=;\n"
+      "DONE%=:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity), "n"(kTries)
+      : "memory");
+  return ok != 0;
 }
-__device__ __forceinline__ bool wait_warp(uint64_t &bar, uint32_t parity, Bars *s, int32_t *status) {
-  return __all_sync(~0u, wait(bar, parity, s, status));
+// The same for a whole warp; a wait that gives up stores WKV_ERR_TIMEOUT and
+// ends its role.
+__device__ __forceinline__ bool wait_warp(uint64_t &bar, uint32_t parity, Bars *, int32_t *status) {
+  const bool ok = __all_sync(~0u, spin(smem_addr(&bar), parity));
+  if (!ok && status) *status = -5;  // WKV_ERR_TIMEOUT
+  return ok;
+}
+// One arrival for a whole warp, behind what its lanes have done.
+__device__ __forceinline__ void arrive_warp(uint64_t &bar) {
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 s;\n setp.eq.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 s, [%0];\n}\n" ::"r"(
+          smem_addr(&bar)),
+      "r"(threadIdx.x & 31u)
+      : "memory");
 }
 
 // The chunks of this CTA's segment, in the pass's order.
@@ -212,209 +273,241 @@ struct Chunks {
   __device__ __forceinline__ int valid(int it) const { return (int)min((int64_t)kL, t1 - start(it)); }
 };
 
-// State warpgroups: R at the chunk's start -> its bfloat16 copy in shared
-// memory and, decayed, tensor memory again; then the weighted keys.
 // Whether the state after the segment goes anywhere; if not, its last chunk
 // adds nothing to it.
 template <bool OUT>
 __device__ __forceinline__ bool wants_state(const Pass &p) {
   return !OUT || (p.nseg == 1 && p.s_out);
 }
+// State warpgroup: R at the chunk's start -> its bfloat16 copy in shared memory
+// and, decayed, tensor memory again.  A thread is a row of the state.
 template <int XP, int YP, bool OUT>
-__device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int64_t bh,
-                                           int terms, float g, float g2) {
-  using Ti = Tiles<XP, YP>;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int x = 32 * (warp & 3) + lane;      // state row (tensor-memory lane)
-  const int y0 = (warp >> 2) * (YP / 2);     // first of this thread's YP / 2 columns
-  const uint32_t tm = s->tmem + 128 + 2 * YP + ((uint32_t)(32 * (warp & 3)) << 16) + y0;
-  const bool rows = 32 * (warp & 3) < XP;    // this warp's lanes hold state rows
+__device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int64_t unit, float g) {
+  using Ti = Tiles<XP, YP, OUT>;
+  const int x = threadIdx.x, warp = x >> 5;
+  const int64_t bh = unit / p.nseg;
+  const uint32_t tm = s->tmem + 128 + 2 * YP + ((uint32_t)(32 * warp) << 16);
+  const bool rows = 32 * warp < XP;  // this warp's lanes hold state rows
   const int64_t XY = (int64_t)p.X * p.Y;
-  const float *init = !OUT ? nullptr : p.nseg > 1 ? p.seg + (bh * p.nseg + blockIdx.x % p.nseg) * XY
-                                     : p.s_in ? p.s_in + bh * XY : nullptr;
+  const float *init = !OUT ? nullptr : p.nseg > 1 ? p.seg + unit * XY : p.s_in ? p.s_in + bh * XY : nullptr;
   const bool init_t = p.nseg == 1 && p.s_in_t;
-  float *result = !OUT ? p.seg + (bh * p.nseg + blockIdx.x % p.nseg) * XY
-                       : wants_state<OUT>(p) ? p.s_out + bh * XY : nullptr;
-  auto store_row = [&](int yb, const uint32_t(&v)[32]) {  // columns yb.. of row x
-    if (x >= p.X) return;
-    float *dst = result + (int64_t)x * p.Y + yb;
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (yb + 4 * q < p.Y) reinterpret_cast<uint4 *>(dst)[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-  };
+  float *result = !OUT ? p.seg + unit * XY : wants_state<OUT>(p) ? p.s_out + bh * XY : nullptr;
   auto load_row = [&](int yb, uint32_t(&v)[32]) {
+    if (!init || x >= p.X) {
 #pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      const int y = yb + q;
-      v[q] = init && x < p.X && y < p.Y ? __float_as_uint(init[init_t ? (int64_t)y * p.X + x : (int64_t)x * p.Y + y]) : 0u;
+      for (int q = 0; q < 32; ++q) v[q] = 0u;
+    } else if (init_t) {
+#pragma unroll
+      for (int q = 0; q < 32; ++q) v[q] = yb + q < p.Y ? __float_as_uint(init[(int64_t)(yb + q) * p.X + x]) : 0u;
+    } else {
+      const uint4 *src = reinterpret_cast<const uint4 *>(init + (int64_t)x * p.Y + yb);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint4 f = yb + 4 * q < p.Y ? src[q] : make_uint4(0u, 0u, 0u, 0u);
+        v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
+      }
     }
   };
-  bool ok = true;
-  for (int it = 0; it < ch.n && ok; ++it) {
-    const int nv = ch.valid(it);
-    const uint32_t ph = it & 1;
-    if (it > 0 && !(ok = wait_warp(s->state, ph ^ 1u, s, p.status))) break;
-    if (OUT) {
+  if (OUT) {
+    if (rows && ch.n > 0) {
+#pragma unroll 1
+      for (int yb = 0; yb < YP; yb += 32) {
+        uint32_t v[32];
+        load_row(yb, v);
+        tmem_st32(tm + yb, v);
+      }
+      tmem_wait_st();
+    }
+#pragma unroll 1
+    for (int it = 0; it < ch.n; ++it) {
+      if (it > 0 && !wait_warp(s->state, (it - 1) & 1, s, p.status)) return;
       if (rows) {
-        const Decay d = decay_of(g, nv);
+        const Decay d = decay_of(g, ch.valid(it));
+        const f2 dm = both(d.m);
         tc_after_sync();
-#pragma unroll
-        for (int blk = 0; blk < YP / 64; ++blk) {
-          const int yb = y0 + 32 * blk;
+#pragma unroll 1
+        for (int yb = 0; yb < YP; yb += 32) {
           uint32_t v[32];
-          if (it == 0) {
-            load_row(yb, v);
-          } else {
-            tmem_ld32_nowait(tm + 32 * blk, v);
-            tmem_wait_ld();
-            pin(v);
-          }
+          tmem_ld32_nowait(tm + yb, v);
+          tmem_wait_ld();
+          pin(v);
           uint8_t *half = sm + Ti::R + (yb >> 6) * (XP * 128);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const float *f = reinterpret_cast<const float *>(v) + 8 * u;
+            const uint32_t *f = v + 8 * u;
             *reinterpret_cast<uint4 *>(half + sw128(x, ((yb & 63) >> 3) + u)) =
-                make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+                make_uint4(pack2(pair_at(f)), pack2(pair_at(f + 2)), pack2(pair_at(f + 4)), pack2(pair_at(f + 6)));
           }
 #pragma unroll
-          for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(decayed(__uint_as_float(v[q]), d));
-          tmem_st32(tm + 32 * blk, v);
+          for (int q = 0; q < 32; q += 2) {  // decayed(), by pairs
+            const f2 z = pair_at(v + q);
+            const float2 r = unpair(fma2(z, dm, d.near_one ? z : 0ull));
+            v[q] = __float_as_uint(r.x), v[q + 1] = __float_as_uint(r.y);
+          }
+          tmem_st32(tm + yb, v);
         }
         tmem_wait_st();
         tc_before_sync();
         fence_proxy_async_smem();
       }
-      mbar_arrive(smem_addr(&s->r_ready));
-      if (!(ok = wait_warp(s->scores, ph, s, p.status))) break;  // b is no longer read as it came
-    }
-    // weighted keys: row j = t % 128, one half of its columns
-    const int st = it % Ti::NB, cst = it % Ti::NC;
-    if (!(ok = wait_warp(s->b_full[st], (it / Ti::NB) & 1, s, p.status))) break;
-    const bool keys = wants_state<OUT>(p) || it + 1 < ch.n;
-    const int j = t & 127;
-    const int64_t n = p.reverse ? j + 1 + (OUT ? 0 : ch.start(it) - ch.t0)
-                                : (OUT ? nv : ch.t1 - ch.start(it)) - 1 - j;
-    const float w = j < nv ? p.sk * power(g2, n) : 0.f;
-    constexpr int UN = XP / 16;  // 16-byte units per thread
-    uint32_t third[4 * UN];
-    uint8_t *tb = sm + Ti::B + st * Ti::BT, *t2 = sm + Ti::W2;
-    const uint32_t hoff = XP == 128 ? (uint32_t)(t >> 7) * kHalf : 0u;
-    const int u0 = XP == 128 ? 0 : (t >> 7) * UN;
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      if (!keys) break;
-      const uint32_t off = hoff + sw128(j, u0 + u);
-      const uint4 in = *reinterpret_cast<const uint4 *>(tb + off);
-      const uint32_t iw[4] = {in.x, in.y, in.z, in.w};
-      uint32_t w1[4], w2[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // rows behind the last position may hold anything: select, not multiply
-        float x0 = j < nv ? lo16(iw[e]) * w : 0.f, x1 = j < nv ? hi16(iw[e]) * w : 0.f;
-        w1[e] = pack2(x0, x1);
-        x0 -= lo16(w1[e]), x1 -= hi16(w1[e]);
-        w2[e] = pack2(x0, x1);
-        x0 -= lo16(w2[e]), x1 -= hi16(w2[e]);
-        third[4 * u + e] = pack2(x0, x1);
-      }
-      *reinterpret_cast<uint4 *>(tb + off) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-      *reinterpret_cast<uint4 *>(t2 + off) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-    }
-    if (nv < kL) {  // c's rows behind the last position: 0 x anything has to be 0
-      if (!(ok = wait_warp(s->c_full[cst], (it / Ti::NC) & 1, s, p.status))) break;
-      uint8_t *tc = sm + Ti::C + cst * Ti::CT;
-      for (int e = t; e < (int)(Ti::CT / 16); e += kStateThreads)
-        if (((e >> 3) & 127) >= nv) reinterpret_cast<uint4 *>(tc)[e] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    fence_proxy_async_smem();
-    mbar_arrive(smem_addr(&s->w_ready));
-    if (keys && terms == 3) {
-      if (!(ok = wait_warp(s->w1_done, ph, s, p.status))) break;
-#pragma unroll
-      for (int u = 0; u < UN; ++u)
-        *reinterpret_cast<uint4 *>(tb + hoff + sw128(j, u0 + u)) =
-            make_uint4(third[4 * u], third[4 * u + 1], third[4 * u + 2], third[4 * u + 3]);
-      fence_proxy_async_smem();
-      mbar_arrive(smem_addr(&s->w3_ready));
+      arrive_warp(s->r_ready);
     }
   }
-  if (!ok || !result || !rows) return;
+  if (!result || !rows) return;
   if (ch.n > 0) {
-    if (!wait_warp(s->state, (ch.n - 1) & 1, s, p.status)) return;
+    if (!wait_warp(s->state, OUT ? (ch.n - 1) & 1 : 0, s, p.status)) return;
     tc_after_sync();
   }
-#pragma unroll
-  for (int blk = 0; blk < YP / 64; ++blk) {
+#pragma unroll 1
+  for (int yb = 0; yb < YP; yb += 32) {
     uint32_t v[32];
     if (ch.n > 0) {
-      tmem_ld32_nowait(tm + 32 * blk, v);
+      tmem_ld32_nowait(tm + yb, v);
       tmem_wait_ld();
       pin(v);
     } else {
-      load_row(y0 + 32 * blk, v);  // no positions: the state goes through
+      load_row(yb, v);  // no positions: the state goes through
     }
-    store_row(y0 + 32 * blk, v);
+    float *dst = result + (int64_t)x * p.Y + yb;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (x < p.X && yb + 4 * q < p.Y) reinterpret_cast<uint4 *>(dst)[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    __syncwarp();
   }
 }
 
-// P warpgroup: masked, weighted scores -> bfloat16 in tensor memory, over the
-// scores' own columns (a thread reads 32 columns before it writes 16 of them).
-__device__ __forceinline__ void scores_role(const Pass &p, Bars *s, const Chunks &ch, float g2) {
-  const int i = threadIdx.x & 127, w = i >> 5, lane = i & 31;
-  const uint32_t tm = s->tmem + ((uint32_t)(32 * w) << 16);
-  const float f = p.si * p.sk;
-  for (int it = 0; it < ch.n; ++it) {
+// P and key warpgroups.  P: the masked, weighted scores, rounded to bfloat16, in
+// tensor memory over the scores' own columns; a thread has a row and half its
+// columns, and the halves' P lies at columns 0 and 64.  Keys: lam^n b, as one
+// bfloat16 term or two that pass through two buffers; a thread has a row
+// (position) and half its columns.
+template <int XP, int YP, bool OUT>
+__device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int terms, float g2) {
+  using Ti = Tiles<XP, YP, OUT>;
+  const int t = threadIdx.x - 32 * Roles<OUT>::KEYS, j = t & 127;
+  constexpr int UN = XP / 16;  // 16-byte units per thread
+  const uint32_t hoff = XP == 128 ? (uint32_t)(t >> 7) * kHalf : 0u;
+  const int u0 = XP == 128 ? 0 : (t >> 7) * UN;
+  int term = 0;  // terms so far
+  // One term of a chunk: f of every pair of the tile at src.
+  auto convert = [&](uint8_t *src, auto f) {
+    const int buf = term & 1;
+    if (term >= 2 && !wait_warp(s->w_free[buf], ((term >> 1) - 1) & 1, s, p.status)) return false;
+    uint8_t *dst = sm + Ti::W + buf * Ti::BT + hoff;
+#pragma unroll 2
+    for (int u = u0; u < u0 + UN; ++u) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(src + sw128(j, u));
+      *reinterpret_cast<uint4 *>(dst + sw128(j, u)) = make_uint4(f(x.x), f(x.y), f(x.z), f(x.w));
+    }
+    fence_proxy_async_smem();
+    arrive_warp(s->w_full[buf]);
+    ++term;
+    return true;
+  };
+  auto keys = [&](int it) {
     const int nv = ch.valid(it);
-    if (!wait_warp(s->scores, it & 1, s, p.status)) return;
+    const int nc = Ti::PER * it + Ti::PER - 1, nb = nc - 1;
+    const bool wanted = wants_state<OUT>(p) || it + 1 < ch.n;
+    uint8_t *src = sm + Ti::RING + nb % Ti::NS * Ti::SLOT + hoff;
+    if (wanted && !wait_warp(s->full[nb % Ti::NS], (nb / Ti::NS) & 1, s, p.status)) return false;
+    if (nv < kL) {  // rows behind the last position may hold anything: 0 x anything has to be 0
+      if (!wait_warp(s->full[nc % Ti::NS], (nc / Ti::NS) & 1, s, p.status)) return false;
+      if (wanted && j >= nv)
+        for (int u = u0; u < u0 + UN; ++u) *reinterpret_cast<uint4 *>(src + sw128(j, u)) = make_uint4(0u, 0u, 0u, 0u);
+      uint8_t *tc = sm + Ti::RING + nc % Ti::NS * Ti::SLOT;
+#pragma unroll 1
+      for (int e = t; e < (int)(Ti::CT / 16); e += kKeyThreads)
+        if (((e >> 3) & 127) >= nv) reinterpret_cast<uint4 *>(tc)[e] = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+      arrive_warp(s->c_clean);
+    }
+    if (!wanted) return true;
+    const int64_t n = p.reverse ? j + 1 + (OUT ? 0 : ch.start(it) - ch.t0)
+                                : (OUT ? nv : ch.t1 - ch.start(it)) - 1 - j;
+    const float w = j < nv ? p.sk * power(g2, n) : 0.f;
+    // the weight in two bfloat16 parts; fma rounds once
+    const uint32_t w1 = pack2(w, w), w2 = pack2(w - lo16(w1), w - lo16(w1));
+    if (terms == 1) return convert(src, [&](uint32_t x) { return fmab(w1, x, mulb(w2, x)); });
+    // second term, negated: what the rounding of the first leaves is exact
+    const uint32_t m1 = w1 ^ 0x80008000u, m2 = w2 ^ 0x80008000u;
+    return convert(src, [&](uint32_t x) { return mulb(w1, x); }) &&
+           convert(src, [&](uint32_t x) { return fmab(m2, x, fmab(m1, x, mulb(w1, x))); });
+  };
+  const int w = (t >> 5) & 3, lane = t & 31, i = 32 * w + lane, half = t >> 7;
+  const uint32_t tm = s->tmem + ((uint32_t)(32 * w) << 16) + 64 * half;
+  const float f = p.si * p.sk;
+  const bool moderate = g2 * 31.f > -100.f;
+  const float *tab = p.reverse ? s->up : s->down;
+  auto scores = [&](int it) {
+    const int nv = ch.valid(it);
+    if (!wait_warp(s->scores, it & 1, s, p.status)) return false;
     tc_after_sync();
 #pragma unroll 1
-    for (int b = 0; b < 4; ++b) {
-      uint32_t out[16];
-      if (p.reverse ? b < w || 32 * b >= nv : b > w) {
+    for (int k = 0; k < 4; ++k) {  // 16 columns from c0 on
+      const int c0 = 64 * half + 16 * k, cb = c0 >> 5;
+      uint32_t out[8];
+      if (p.reverse ? cb < w || c0 >= nv : cb > w) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) out[r] = 0u;
+        for (int r = 0; r < 8; ++r) out[r] = 0u;
       } else {
-        uint32_t v[32];
-        tmem_ld32_nowait(tm + 32 * b, v);
+        uint32_t v[16];
+        tmem_ld16_nowait(tm + 16 * k, v);
+        // lam^{|i-j|} as a factor of the row and one of the column (by blocks
+        // of 32 columns); on the diagonal the row's is up to lam^{-31}, so
+        // strong decays take the product from a table there
+        const bool diag = cb == w;
+        const f2 e = both(f * ex2(g2 * (float)(p.reverse ? 32 * cb - i : i - 32 * cb - 31)));
+        const int q0 = c0 & 16;
         tmem_wait_ld();
         pin(v);
-        if (b == w) {  // the diagonal
-          const int last = p.reverse ? nv - 32 * b : 32;
+        if (nv - c0 < 16) {  // columns behind the last position may hold anything
 #pragma unroll
-          for (int r = 0; r < 32; ++r) {
-            const int n = p.reverse ? r - lane : lane - r;
-            v[r] = __float_as_uint(n >= 0 && r < last ? __uint_as_float(v[r]) * (f * s->up[n & 31]) : 0.f);
+          for (int r = 0; r < 16; ++r) v[r] = c0 + r < nv ? v[r] : 0u;
+        }
+        if (diag && !moderate) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const int n0 = p.reverse ? q0 + 2 * r - lane : lane - 2 * r - q0, n1 = p.reverse ? n0 + 1 : n0 - 1;
+            out[r] = pack2(n0 >= 0 ? __uint_as_float(v[2 * r]) * (f * s->up[n0 & 31]) : 0.f,
+                           n1 >= 0 ? __uint_as_float(v[2 * r + 1]) * (f * s->up[n1 & 31]) : 0.f);
           }
         } else {
-          const float e = f * ex2(g2 * (float)(p.reverse ? 32 * b - i : i - 32 * b - 31));
-          const float *tab = p.reverse ? s->up : s->down;
-          const int last = p.reverse ? nv - 32 * b : 32;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 z = *reinterpret_cast<const float4 *>(tab + 4 * q);
-            v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) * (e * z.x));
-            v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) * (e * z.y));
-            v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) * (e * z.z));
-            v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) * (e * z.w));
+          for (int q = 0; q < 4; ++q) {
+            const ulonglong2 z = *reinterpret_cast<const ulonglong2 *>(tab + q0 + 4 * q);
+            out[2 * q] = pack2(mul2(pair_at(v + 4 * q), mul2(e, z.x)));
+            out[2 * q + 1] = pack2(mul2(pair_at(v + 4 * q + 2), mul2(e, z.y)));
           }
-          if (last < 32) {
+          if (diag) {
+            // pairs (2 r, 2 r + 1) against the row: kept, half kept, dropped;
+            // columns kept, from the last (first) on
+            const int d = p.reverse ? 16 + q0 - lane : lane + 1 - q0;
 #pragma unroll
-            for (int r = 0; r < 32; ++r) v[r] = r < last ? v[r] : 0u;
+            for (int r = 0; r < 8; ++r) {
+              const int m = d - (p.reverse ? 14 - 2 * r : 2 * r);
+              out[r] = m >= 2 ? out[r] : m == 1 ? out[r] & (p.reverse ? 0xFFFF0000u : 0xFFFFu) : 0u;
+            }
           }
         }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) out[r] = pack2(__uint_as_float(v[2 * r]), __uint_as_float(v[2 * r + 1]));
       }
-      tmem_st16(tm + 16 * b, out);
+      tmem_st8(tm + 8 * k, out);
     }
     tmem_wait_st();
     tc_before_sync();
-    mbar_arrive(smem_addr(&s->p_ready));
+    arrive_warp(s->p_ready);
+    return true;
+  };
+#pragma unroll 1
+  for (int it = -1; it < ch.n; ++it) {
+    if (it >= 0) {
+      if (OUT && !scores(it)) return;
+    }
+    if (it + 1 < ch.n && !keys(it + 1)) return;
   }
 }
 
-// Output warpgroup: P c + weight x (a R), one row per thread, rounded and
-// stored as 16- or 32-byte pieces of its row.
+// Output warpgroup, a thread per row: P c + weight x (a R), rounded and stored
+// as 16- or 32-byte pieces of the row.
 template <int YP>
 __device__ __forceinline__ void output_role(const Pass &p, Bars *s, const Chunks &ch, int64_t b, int64_t h, float g2,
                                             bool wide) {
@@ -422,185 +515,201 @@ __device__ __forceinline__ void output_role(const Pass &p, Bars *s, const Chunks
   const uint32_t tm = s->tmem + 128 + ((uint32_t)(i & ~31) << 16);
   for (int it = 0; it < ch.n; ++it) {
     const int nv = ch.valid(it);
-    if (!wait_warp(s->o_done, it & 1, s, p.status)) return;
-    tc_after_sync();
-    const float w = i < nv ? p.si * power(g2, p.reverse ? nv - 1 - i : i + 1) : 0.f;
+    const f2 w = both(i < nv ? p.si * power(g2, p.reverse ? nv - 1 - i : i + 1) : 0.f);
     const int64_t t = ch.start(it) + i;
     uint16_t *dst = static_cast<uint16_t *>(const_cast<void *>(p.o.p)) + b * p.o.sb + h * p.o.sh + t * p.o.st;
-#pragma unroll
-    for (int blk = 0; blk < YP / 32; ++blk) {
-      uint32_t o1[32], o2[32], out[16];
-      tmem_ld32_nowait(tm + 32 * blk, o1);
-      tmem_ld32_nowait(tm + YP + 32 * blk, o2);
+    if (!wait_warp(s->o_done, it & 1, s, p.status)) return;
+    tc_after_sync();
+#pragma unroll 1
+    for (int y = 0; y < YP; y += 16) {
+      uint32_t o1[16], o2[16], z[8];
+      tmem_ld16_nowait(tm + y, o1);
+      tmem_ld16_nowait(tm + YP + y, o2);
       tmem_wait_ld();
       pin(o1);
       pin(o2);
-      if (blk == YP / 32 - 1) {
+      if (y == YP - 16) {
         tc_before_sync();
-        mbar_arrive(smem_addr(&s->o_free));
+        arrive_warp(s->o_free);
       }
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        out[r] = i < nv ? pack2(fmaf(w, __uint_as_float(o2[2 * r]), __uint_as_float(o1[2 * r])),
-                                fmaf(w, __uint_as_float(o2[2 * r + 1]), __uint_as_float(o1[2 * r + 1])))
-                        : 0u;
-      if (t >= p.T) continue;
-      if (wide) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (32 * blk + 16 * q < p.Y)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 32 * blk + 16 * q),
-                         "r"(out[8 * q]), "r"(out[8 * q + 1]), "r"(out[8 * q + 2]), "r"(out[8 * q + 3]),
-                         "r"(out[8 * q + 4]), "r"(out[8 * q + 5]), "r"(out[8 * q + 6]), "r"(out[8 * q + 7])
-                         : "memory");
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (32 * blk + 8 * q < p.Y)
-            *reinterpret_cast<uint4 *>(dst + 32 * blk + 8 * q) =
-                make_uint4(out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]);
+      for (int r = 0; r < 8; ++r) {
+        z[r] = pack2(fma2(w, pair_at(o2 + 2 * r), pair_at(o1 + 2 * r)));
+        if (i >= nv) z[r] = 0u;
       }
+      if (t < p.T && wide) {
+        if (y < p.Y)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + y), "r"(z[0]), "r"(z[1]),
+                       "r"(z[2]), "r"(z[3]), "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
+                       : "memory");
+      } else if (t < p.T) {
+        if (y < p.Y) *reinterpret_cast<uint4 *>(dst + y) = make_uint4(z[0], z[1], z[2], z[3]);
+        if (y + 8 < p.Y) *reinterpret_cast<uint4 *>(dst + y + 8) = make_uint4(z[4], z[5], z[6], z[7]);
+      }
+      __syncwarp();
     }
   }
 }
 
-// Loads: b and c of a chunk, then a, each as soon as its stage is free.
+// Loads: the tiles of each chunk in the ring's order, each as soon as its slot
+// is free; one whole warp.
 template <int XP, int YP, bool OUT>
 __device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, int b, int h,
                                           const CUtensorMap *am, const CUtensorMap *bm, const CUtensorMap *cm) {
-  using Ti = Tiles<XP, YP>;
-  auto tile = [&](uint32_t dst, const CUtensorMap *m, uint64_t &full, uint32_t bytes, int64_t t) {
-    const uint32_t bar = smem_addr(&full);
-    mbar_expect_tx(bar, bytes);
-    for (uint32_t o = 0; o < bytes; o += kHalf) tma_load_4d(dst + o, m, (int)(o / kHalf) * 64, (int)t, h, b, bar);
-  };
-  int nb = 0, nc = 0, na = 0;  // tiles whose loads were issued
-  bool ok = true;
-  for (int it = 0; it < ch.n && ok; ++it) {
-    const int64_t t = ch.start(it);
-    int st = it % Ti::NB;
-    if (it >= Ti::NB && !(ok = wait(s->b_empty[st], (it / Ti::NB - 1) & 1, s, p.status))) break;
-    tile(sm + Ti::B + st * Ti::BT, bm, s->b_full[st], Ti::BT, t);
-    nb = it + 1;
-    st = it % Ti::NC;
-    if (it >= Ti::NC && !(ok = wait(s->c_empty[st], (it / Ti::NC - 1) & 1, s, p.status))) break;
-    tile(sm + Ti::C + st * Ti::CT, cm, s->c_full[st], Ti::CT, t);
-    nc = it + 1;
-    if (OUT) {
-      st = it % Ti::NA;
-      if (it >= Ti::NA && !(ok = wait(s->a_empty[st], (it / Ti::NA - 1) & 1, s, p.status))) break;
-      tile(sm + Ti::A + st * Ti::BT, am, s->a_full[st], Ti::BT, t);
-      na = it + 1;
-    }
-  }
-  // The loads in flight write shared memory that outlives this thread, not the
-  // CTA: every one is waited for (in order to end; consumers wait for theirs).
-  for (int it = max(0, nb - Ti::NB); it < nb; ++it)
-    mbar_wait(smem_addr(&s->b_full[it % Ti::NB]), (it / Ti::NB) & 1, kBudgetNs, nullptr);
-  for (int it = max(0, nc - Ti::NC); it < nc; ++it)
-    mbar_wait(smem_addr(&s->c_full[it % Ti::NC]), (it / Ti::NC) & 1, kBudgetNs, nullptr);
-  for (int it = max(0, na - Ti::NA); it < na; ++it)
-    mbar_wait(smem_addr(&s->a_full[it % Ti::NA]), (it / Ti::NA) & 1, kBudgetNs, nullptr);
-}
-
-// MMAs, in an order that gives each warpgroup's step the products of another
-// to hide behind: a R and P c, then the state's products, then the next
-// chunk's scores while the state's copy is made.
-template <int XP, int YP, bool OUT>
-__device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, int terms) {
-  using Ti = Tiles<XP, YP>;
-  constexpr uint32_t SCORES = 0, O1 = 128, O2 = 128 + YP, ST = 128 + 2 * YP;
-  const uint32_t tm = s->tmem;
-  auto scores = [&](int it) {
-    if (!wait(s->b_full[it % Ti::NB], (it / Ti::NB) & 1, s, p.status)) return false;
-    if (!wait(s->a_full[it % Ti::NA], (it / Ti::NA) & 1, s, p.status)) return false;
-    const uint32_t ta = sm + Ti::A + (it % Ti::NA) * Ti::BT, tb = sm + Ti::B + (it % Ti::NB) * Ti::BT;
-#pragma unroll
-    for (int k = 0; k < XP / 16; ++k) mma_ss(tm + SCORES, kmajor(ta, k), kmajor(tb, k), idesc(128, 128, false, false), k > 0);
-    mma_commit(smem_addr(&s->scores));
-    return true;
-  };
-  bool ok = true;
-  if (OUT && ch.n > 0) ok = scores(0);
-  for (int it = 0; it < ch.n && ok; ++it) {
-    const uint32_t ph = it & 1;
-    const uint32_t ta = sm + Ti::A + (it % Ti::NA) * Ti::BT, tb = sm + Ti::B + (it % Ti::NB) * Ti::BT,
-                   tc = sm + Ti::C + (it % Ti::NC) * Ti::CT;
-    if (OUT) {
-      if (!(ok = wait(s->r_ready, ph, s, p.status))) break;
-      if (it > 0 && !(ok = wait(s->o_free, ph ^ 1u, s, p.status))) break;
-      tc_after_sync();
-#pragma unroll
-      for (int k = 0; k < XP / 16; ++k)
-        mma_ss(tm + O2, kmajor(ta, k), mnmajor(sm + Ti::R, k, XP * 128), idesc(128, YP, false, true), k > 0);
-      mma_commit(smem_addr(&s->a_empty[it % Ti::NA]));
-    }
-    if (!(ok = wait(s->c_full[it % Ti::NC], (it / Ti::NC) & 1, s, p.status))) break;
-    if (!(ok = wait(s->w_ready, ph, s, p.status))) break;
-    if (OUT) {
-      if (!(ok = wait(s->p_ready, ph, s, p.status))) break;
-      tc_after_sync();
-#pragma unroll
-      for (int k = 0; k < kL / 16; ++k)
-        mma_ts(tm + O1, tm + SCORES + 8 * k, mnmajor(tc, k, kHalf), idesc(128, YP, false, true), k > 0);
-      mma_commit(smem_addr(&s->o_done));
-    }
-    tc_after_sync();
-    const bool keys = wants_state<OUT>(p) || it + 1 < ch.n;
-    for (int term = 0; keys && term < terms; ++term) {
-      if (term == 2 && !(ok = wait(s->w3_ready, ph, s, p.status))) break;
-      const uint32_t tw = term == 1 ? sm + Ti::W2 : tb;
-#pragma unroll
-      for (int k = 0; k < kL / 16; ++k)
-        mma_ss(tm + ST, mnmajor(tw, k, kHalf), mnmajor(tc, k, kHalf), idesc(128, YP, true, true), OUT || it > 0 || term > 0 || k > 0);
-      if (term == 0 && terms == 3) mma_commit(smem_addr(&s->w1_done));
+  using Ti = Tiles<XP, YP, OUT>;
+  int n = 0;  // tiles whose loads were issued
+  for (int it = 0; it < ch.n; ++it) {
+    const int t = (int)ch.start(it);
+    bool ok = true;
+    for (int k = 0; k < Ti::PER; ++k) {
+      const int slot = n % Ti::NS;
+      if (n >= Ti::NS && !(ok = wait_warp(s->empty[slot], (n / Ti::NS - 1) & 1, s, p.status))) break;
+      const bool is_c = k == Ti::PER - 1;
+      const CUtensorMap *m = is_c ? cm : k == Ti::PER - 2 ? bm : am;
+      const uint32_t bytes = is_c ? Ti::CT : Ti::BT, dst = sm + Ti::RING + slot * Ti::SLOT, bar = smem_addr(&s->full[slot]);
+      if (elect_one()) {
+        mbar_expect_tx(bar, bytes);
+        for (uint32_t o = 0; o < bytes; o += kHalf) tma_load_4d(dst + o, m, (int)(o / kHalf) * 64, t, h, b, bar);
+      }
+      __syncwarp();
+      ++n;
     }
     if (!ok) break;
-    mma_commit(smem_addr(&s->state));
-    mma_commit(smem_addr(&s->b_empty[it % Ti::NB]));
-    mma_commit(smem_addr(&s->c_empty[it % Ti::NC]));
-    if (OUT && it + 1 < ch.n) ok = scores(it + 1);
+  }
+  // The loads in flight write shared memory that outlives this warp, not the
+  // CTA: every one is waited for (in order to end; consumers wait for theirs).
+  if (elect_one())
+    for (int k = max(0, n - Ti::NS); k < n; ++k) spin(smem_addr(&s->full[k % Ti::NS]), (k / Ti::NS) & 1);
+}
+
+// MMAs, in the order that the head of this file explains; one whole warp.
+template <int XP, int YP, bool OUT>
+__device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, int terms) {
+  using Ti = Tiles<XP, YP, OUT>;
+  constexpr uint32_t SCORES = 0, O1 = 128, O2 = 128 + YP, ST = 128 + 2 * YP;
+  const uint32_t tm = __shfl_sync(~0u, s->tmem, 0);
+  auto loaded = [&](int n) { return wait_warp(s->full[n % Ti::NS], (n / Ti::NS) & 1, s, p.status); };
+  auto tile = [&](int n) { return sm + Ti::RING + n % Ti::NS * Ti::SLOT; };
+  int term = 0;  // terms of the keys so far
+  bool ok = true;
+#pragma unroll 1
+  for (int it = 0; it < ch.n; ++it) {
+    const uint32_t ph = it & 1;
+    const int na = Ti::PER * it, nc = na + Ti::PER - 1, nb = nc - 1;
+    const uint32_t ta = tile(na), tb = tile(nb), tc = tile(nc);
+    const int n_terms = wants_state<OUT>(p) || it + 1 < ch.n ? terms : 0;
+    if (OUT) {
+      if (!(ok = loaded(nb) && loaded(na))) break;
+      if (elect_one()) {
+        const uint64_t da = kmajor(ta), db = kmajor(tb);
+#pragma unroll
+        for (int k = 0; k < XP / 16; ++k) mma_ss(tm + SCORES, da + kstep(k), db + kstep(k), idesc(128, 128, false, false), k > 0);
+        mma_commit(smem_addr(&s->scores));
+      }
+      __syncwarp();
+      if (!(ok = wait_warp(s->r_ready, ph, s, p.status))) break;
+    }
+    if (!(ok = loaded(nc))) break;
+    if (ch.valid(it) < kL && !(ok = wait_warp(s->c_clean, 0, s, p.status))) break;
+    // the keys' terms, and a R behind the first of them
+#pragma unroll 1
+    for (int k = 0; k < max(n_terms, 1); ++k) {
+      if (n_terms > 0) {
+        const int buf = term & 1;
+        if (!(ok = wait_warp(s->w_full[buf], (term >> 1) & 1, s, p.status))) break;
+        tc_after_sync();
+        if (elect_one()) {
+          const uint64_t dw = mnmajor(sm + Ti::W + buf * Ti::BT, kHalf), dc = mnmajor(tc, kHalf);
+          const bool acc = OUT || it > 0 || k > 0;
+          const uint32_t id = idesc(128, YP, true, true) | (k > 0 ? kNegateA : 0u);
+#pragma unroll
+          for (int i = 0; i < kL / 16; ++i)
+            mma_ss(tm + ST, dw + mnstep(i), dc + mnstep(i), id, acc || i > 0);
+          mma_commit(smem_addr(&s->w_free[buf]));
+        }
+        __syncwarp();
+        ++term;
+      }
+      if (OUT && k == 0) {
+        if (it > 0 && !(ok = wait_warp(s->o_free, ph ^ 1u, s, p.status))) break;
+        tc_after_sync();
+        if (elect_one()) {
+          const uint64_t da = kmajor(ta), dr = mnmajor(sm + Ti::R, XP * 128);
+#pragma unroll
+          for (int i = 0; i < XP / 16; ++i)
+            mma_ss(tm + O2, da + kstep(i), dr + mnstep(i), idesc(128, YP, false, true), i > 0);
+          mma_commit(smem_addr(&s->empty[na % Ti::NS]));
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) break;
+    if (elect_one()) {
+      if (n_terms > 0 && (OUT || it + 1 == ch.n)) mma_commit(smem_addr(&s->state));
+      // the last term's arrival said that b was read, too
+      if (OUT) mma_commit(smem_addr(&s->empty[nb % Ti::NS]));
+      else mbar_arrive(smem_addr(&s->empty[nb % Ti::NS]));
+    }
+    __syncwarp();
+    if (OUT) {
+      if (!(ok = wait_warp(s->p_ready, ph, s, p.status))) break;
+      tc_after_sync();
+    }
+    if (elect_one()) {
+      if (OUT) {
+        const uint64_t dc = mnmajor(tc, kHalf);
+#pragma unroll
+        for (int k = 0; k < kL / 16; ++k)
+          mma_ts(tm + O1, tm + SCORES + 8 * k + (k >= 4 ? 32 : 0), dc + mnstep(k), idesc(128, YP, false, true), k > 0);
+        mma_commit(smem_addr(&s->o_done));
+      }
+      mma_commit(smem_addr(&s->empty[nc % Ti::NS]));
+    }
+    __syncwarp();
   }
   // MMAs in flight read shared memory and write tensor memory: they end before the CTA does
-  mma_commit(smem_addr(&s->drain));
-  mbar_wait(smem_addr(&s->drain), 0, kBudgetNs, nullptr);
+  if (elect_one()) mma_commit(smem_addr(&s->drain));
+  __syncwarp();
+  if (elect_one()) spin(smem_addr(&s->drain), 0);
 }
 
 struct Maps {
   CUtensorMap a[3], b[3], c[3];
   int terms[3], wide[3];
 };
+// A block is a segment of a head of one pass; the passes of a segment are
+// neighbours, so that those that read the same tensors find them in L2.
 template <int XP, int YP, bool OUT>
-__global__ void __launch_bounds__(OUT ? 576 : 320, 1) decay_tc_kernel(const __grid_constant__ Maps maps,
-                                                                      const __grid_constant__ Group group) {
-  const Pass &p = group.p[blockIdx.y];
-  const CUtensorMap &am = maps.a[blockIdx.y], &bm = maps.b[blockIdx.y], &cm = maps.c[blockIdx.y];
-  const int terms = maps.terms[blockIdx.y], wide = maps.wide[blockIdx.y];
-  if (!OUT && !p.scan_out && (int)blockIdx.x % p.nseg == (p.reverse ? 0 : p.nseg - 1)) return;  // no state starts from it
+__global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const __grid_constant__ Maps maps,
+                                                                          const __grid_constant__ Group group) {
+  using Ro = Roles<OUT>;
+  const int pass = (int)(blockIdx.x % (unsigned)group.n);
+  const int64_t unit = blockIdx.x / (unsigned)group.n;
+  const Pass &p = group.p[pass];
+  const CUtensorMap &am = maps.a[pass], &bm = maps.b[pass], &cm = maps.c[pass];
+  const int terms = maps.terms[pass], wide = maps.wide[pass];
+  const int64_t bh = unit / p.nseg, sg = unit % p.nseg, b = bh / p.H, h = bh % p.H;
+  if (!OUT && !p.scan_out && sg == (p.reverse ? 0 : p.nseg - 1)) return;  // no state starts from it
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
   uint8_t *sm = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
-  const int64_t bh = blockIdx.x / p.nseg, b = bh / p.H, h = bh % p.H;
   const int64_t n = row_len(p, b);
   Chunks ch;
-  ch.t0 = (blockIdx.x % p.nseg) * p.seg_len;
+  ch.t0 = sg * p.seg_len;
   const int64_t tz = min(ch.t0 + p.seg_len, p.T);
   ch.t1 = max(ch.t0, min(tz, n));
   ch.c0 = ch.t0 / kL;
   ch.n = (int)((ch.t1 - ch.t0 + kL - 1) / kL);
   ch.reverse = p.reverse;
   const float g = p.log_decay[h], g2 = g * kLog2e;
-  const int warp = threadIdx.x >> 5;
-  constexpr int kLoadWarp = OUT ? 16 : 8;
+  const int warp = __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4; ++i)
-      for (uint64_t *f : {&bars.b_full[i], &bars.c_full[i], &bars.a_full[i], &bars.b_empty[i], &bars.c_empty[i], &bars.a_empty[i]})
-        mbar_init(smem_addr(f), 1);
-    for (uint64_t *f : {&bars.scores, &bars.w1_done, &bars.state, &bars.o_done, &bars.drain}) mbar_init(smem_addr(f), 1);
-    for (uint64_t *f : {&bars.w_ready, &bars.w3_ready, &bars.r_ready}) mbar_init(smem_addr(f), kStateThreads);
-    for (uint64_t *f : {&bars.p_ready, &bars.o_free}) mbar_init(smem_addr(f), 128);
+    for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 1);
+    for (uint64_t *f : {&bars.scores, &bars.w_free[0], &bars.w_free[1], &bars.state, &bars.o_done, &bars.drain})
+      mbar_init(smem_addr(f), 1);
+    for (uint64_t *f : {&bars.w_full[0], &bars.w_full[1], &bars.c_clean, &bars.p_ready}) mbar_init(smem_addr(f), kKeyThreads / 32);
+    for (uint64_t *f : {&bars.o_free, &bars.r_ready}) mbar_init(smem_addr(f), 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    bars.fail = 0;
   }
   if (threadIdx.x >= 32 && threadIdx.x < 64) {
     const int r = threadIdx.x - 32;
@@ -611,16 +720,15 @@ __global__ void __launch_bounds__(OUT ? 576 : 320, 1) decay_tc_kernel(const __gr
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
-  if (warp < kStateThreads / 32) {
-    state_role<XP, YP, OUT>(p, &bars, sm, ch, bh, terms, g, g2);
-  } else if (OUT && warp < 12) {
-    scores_role(p, &bars, ch, g2);
-  } else if (OUT && warp < 16) {
+  if (warp < 4) {
+    state_role<XP, YP, OUT>(p, &bars, sm, ch, unit, g);
+  } else if (OUT && warp < Ro::KEYS) {
     output_role<YP>(p, &bars, ch, b, h, g2, wide != 0);
-  } else if (warp == kLoadWarp) {
-    if ((threadIdx.x & 31) == 0) load_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, (int)b, (int)h, &am, &bm, &cm);
+  } else if (warp < Ro::LOAD) {
+    keys_role<XP, YP, OUT>(p, &bars, sm, ch, terms, g2);
   } else {
-    if ((threadIdx.x & 31) == 0) mma_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, terms);
+    if (warp == Ro::LOAD) load_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, (int)b, (int)h, &am, &bm, &cm);
+    else mma_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, terms);
   }
   __syncwarp();
   if (OUT) {  // chunks without valid positions
@@ -684,9 +792,9 @@ cudaError_t launch_t(const Group &g, cudaStream_t st) {
   Maps m{};
   if (!encoder() || !ensure_context()) return cudaErrorNotSupported;
   const auto kern = decay_tc_kernel<XP, YP, OUT>;
-  constexpr int smem = (int)Tiles<XP, YP>::BYTES + 1024;
+  constexpr int smem = (int)Tiles<XP, YP, OUT>::BYTES + 1024;
   int blocks = 0;
-  const cudaError_t e = blocks_per_sm((const void *)kern, OUT ? 576 : 320, smem, &blocks);
+  const cudaError_t e = blocks_per_sm((const void *)kern, Roles<OUT>::THREADS, smem, &blocks);
   if (e != cudaSuccess) return e;
   if (blocks < 1) return cudaErrorInvalidConfiguration;
   auto even = [](int64_t s, int64_t n) { return n <= 1 || s % 16 == 0; };
@@ -697,10 +805,10 @@ cudaError_t launch_t(const Group &g, cudaStream_t st) {
     m.wide[i] = OUT && ((uintptr_t)p.o.p & 31u) == 0 && p.Y % 16 == 0 && even(p.o.sb, p.B) && even(p.o.st, p.T) &&
                 even(p.o.sh, p.H);
     // states that a call may hand out are float32; those that only meet rows as bfloat16 copies need not be
-    m.terms[i] = p.exact_state && (!OUT || p.nseg == 1) ? 3 : 2;
+    m.terms[i] = p.exact_state && (!OUT || p.nseg == 1) ? 2 : 1;
   }
   const Pass &p = g.p[0];
-  return launch_kernel(kern, dim3((unsigned)(p.B * p.H * p.nseg), (unsigned)g.n), dim3(OUT ? 576 : 320), smem, st, m, g);
+  return launch_kernel(kern, dim3((unsigned)(p.B * p.H * p.nseg * g.n)), dim3(Roles<OUT>::THREADS), smem, st, m, g);
 }
 template <bool OUT>
 cudaError_t launch_o(const Group &g, cudaStream_t st) {
