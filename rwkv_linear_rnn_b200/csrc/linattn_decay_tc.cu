@@ -26,7 +26,8 @@
 //
 // One CTA runs one head's segment with specialised warps: a producer (TMA
 // loads), an MMA issuer, a warpgroup for the state (its bfloat16 copy and its
-// decay), one for the outputs, two for P and the weighted keys.  The MMAs of a
+// decay), one for the outputs, two for P, one for the
+// weighted keys.  The MMAs of a
 // chunk are issued in the order scores, keys (first term), a R, keys (other
 // terms), P c, so that each step of a warpgroup has the products of others to
 // hide behind: P behind keys and a R, the state's step behind P c and the next
@@ -187,7 +188,7 @@ __device__ __forceinline__ uint32_t pack2(f2 v) {
 }
 __device__ __forceinline__ f2 pair_at(const uint32_t *r) { return pair(__uint_as_float(r[0]), __uint_as_float(r[1])); }
 // lam^n for n >= 0 (1 for n = 0 whatever lam is); g2 = log_decay log2(e).
-__device__ __forceinline__ float power(float g2, int64_t n) { return n == 0 ? 1.f : ex2(g2 * (float)n); }
+__device__ __forceinline__ float power(float g2, int n) { return n == 0 ? 1.f : ex2(g2 * (float)n); }
 
 // ------------------------------------------------------------- the pass ---
 // Shared memory: two buffers for the terms of the weighted keys, a ring of NS
@@ -211,9 +212,9 @@ struct Bars {
   uint64_t full[8], empty[8];  // ring slots
   uint64_t scores;             // a b^T complete (MMA)
   uint64_t p_ready;            // P in tensor memory (P warpgroups)
-  uint64_t w_full[2];          // a term of the weighted keys in its buffer (key warpgroups)
+  uint64_t w_full[2];          // a term of the weighted keys in its buffer (key warpgroup)
   uint64_t w_free[2];          // its products complete (MMA)
-  uint64_t c_clean;            // c's rows behind the last position zeroed (key warpgroups; a segment has one such chunk)
+  uint64_t c_clean;            // c's rows behind the last position zeroed (key warpgroup; a segment has one such chunk)
   uint64_t state;              // a R and all products into the state complete (MMA)
   uint64_t r_ready;            // the state's copy in shared memory, the state decayed in tensor memory (state warpgroup)
   uint64_t o_done;             // outputs complete in tensor memory (MMA)
@@ -223,13 +224,14 @@ struct Bars {
   alignas(16) float up[32];  // lam^r, lam^{31-r}; read four at a time
   alignas(16) float down[32];
 };
-constexpr int kKeyThreads = 256;
-// Warps of a CTA: 4 state, (4 outputs,) 8 P and keys, loads, MMAs.  Their hot
+constexpr int kKeyThreads = 128, kScoreWarps = 8;
+// Warps of a CTA: 4 state, (4 outputs, 8 P,) 4 keys, loads, MMAs.  Their hot
 // loops are kept short: one that does not fit the instruction cache with the
-// others waits for its instructions, chunk after chunk.
+// others waits for its instructions, chunk after chunk.  Nor may a register
+// spill: shared memory takes L1's place and a reload is a trip to L2.
 template <bool OUT>
 struct Roles {
-  static constexpr int KEYS = OUT ? 8 : 4, LOAD = KEYS + 8, MMA = LOAD + 1, THREADS = 32 * (MMA + 1);
+  static constexpr int KEYS = OUT ? 16 : 4, LOAD = KEYS + 4, MMA = LOAD + 1, THREADS = 32 * (MMA + 1);
 };
 
 // Waits for the phase of `addr` with the given parity, in at most kTries tries
@@ -265,12 +267,11 @@ __device__ __forceinline__ void arrive_warp(uint64_t &bar) {
 
 // The chunks of this CTA's segment, in the pass's order.
 struct Chunks {
-  int64_t t0, t1;  // the segment's valid positions
-  int64_t c0;      // first chunk
-  int n;           // chunks with valid positions
+  int t0, t1;  // the segment's valid positions
+  int n;       // chunks with valid positions
   bool reverse;
-  __device__ __forceinline__ int64_t start(int it) const { return (c0 + (reverse ? n - 1 - it : it)) * kL; }
-  __device__ __forceinline__ int valid(int it) const { return (int)min((int64_t)kL, t1 - start(it)); }
+  __device__ __forceinline__ int start(int it) const { return t0 + (reverse ? n - 1 - it : it) * kL; }
+  __device__ __forceinline__ int valid(int it) const { return min(kL, t1 - start(it)); }
 };
 
 // Whether the state after the segment goes anywhere; if not, its last chunk
@@ -334,15 +335,15 @@ __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, 
           uint8_t *half = sm + Ti::R + (yb >> 6) * (XP * 128);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const uint32_t *f = v + 8 * u;
+            uint32_t *f = v + 8 * u;
             *reinterpret_cast<uint4 *>(half + sw128(x, ((yb & 63) >> 3) + u)) =
                 make_uint4(pack2(pair_at(f)), pack2(pair_at(f + 2)), pack2(pair_at(f + 4)), pack2(pair_at(f + 6)));
-          }
 #pragma unroll
-          for (int q = 0; q < 32; q += 2) {  // decayed(), by pairs
-            const f2 z = pair_at(v + q);
-            const float2 r = unpair(fma2(z, dm, d.near_one ? z : 0ull));
-            v[q] = __float_as_uint(r.x), v[q + 1] = __float_as_uint(r.y);
+            for (int q = 0; q < 8; q += 2) {  // decayed(), by pairs
+              const f2 z = pair_at(f + q);
+              const float2 r = unpair(fma2(z, dm, d.near_one ? z : 0ull));
+              f[q] = __float_as_uint(r.x), f[q + 1] = __float_as_uint(r.y);
+            }
           }
           tmem_st32(tm + yb, v);
         }
@@ -376,75 +377,90 @@ __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, 
   }
 }
 
-// P and key warpgroups.  P: the masked, weighted scores, rounded to bfloat16, in
-// tensor memory over the scores' own columns; a thread has a row and half its
-// columns, and the halves' P lies at columns 0 and 64.  Keys: lam^n b, as one
-// bfloat16 term or two that pass through two buffers; a thread has a row
-// (position) and half its columns.
+// Key warpgroup: lam^n b, as one bfloat16 term or two that pass through two
+// buffers; a thread has a row (position).
 template <int XP, int YP, bool OUT>
 __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int terms, float g2) {
   using Ti = Tiles<XP, YP, OUT>;
-  const int t = threadIdx.x - 32 * Roles<OUT>::KEYS, j = t & 127;
-  constexpr int UN = XP / 16;  // 16-byte units per thread
-  const uint32_t hoff = XP == 128 ? (uint32_t)(t >> 7) * kHalf : 0u;
-  const int u0 = XP == 128 ? 0 : (t >> 7) * UN;
+  const int j = threadIdx.x - 32 * Roles<OUT>::KEYS;
   int term = 0;  // terms so far
   // One term of a chunk: f of every pair of the tile at src.
   auto convert = [&](uint8_t *src, auto f) {
     const int buf = term & 1;
     if (term >= 2 && !wait_warp(s->w_free[buf], ((term >> 1) - 1) & 1, s, p.status)) return false;
-    uint8_t *dst = sm + Ti::W + buf * Ti::BT + hoff;
-#pragma unroll 2
-    for (int u = u0; u < u0 + UN; ++u) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(src + sw128(j, u));
-      *reinterpret_cast<uint4 *>(dst + sw128(j, u)) = make_uint4(f(x.x), f(x.y), f(x.z), f(x.w));
+    uint8_t *dst = sm + Ti::W + buf * Ti::BT;
+#pragma unroll 1
+    for (uint32_t o = 0; o < Ti::BT; o += kHalf) {
+#pragma unroll
+      for (int v = 0; v < 8; v += 4) {
+        uint4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const uint4 *>(src + o + sw128(j, v + u));
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<uint4 *>(dst + o + sw128(j, v + u)) = make_uint4(f(x[u].x), f(x[u].y), f(x[u].z), f(x[u].w));
+      }
     }
     fence_proxy_async_smem();
     arrive_warp(s->w_full[buf]);
     ++term;
     return true;
   };
-  auto keys = [&](int it) {
+#pragma unroll 1
+  for (int it = 0; it < ch.n; ++it) {
     const int nv = ch.valid(it);
     const int nc = Ti::PER * it + Ti::PER - 1, nb = nc - 1;
     const bool wanted = wants_state<OUT>(p) || it + 1 < ch.n;
-    uint8_t *src = sm + Ti::RING + nb % Ti::NS * Ti::SLOT + hoff;
-    if (wanted && !wait_warp(s->full[nb % Ti::NS], (nb / Ti::NS) & 1, s, p.status)) return false;
+    uint8_t *src = sm + Ti::RING + nb % Ti::NS * Ti::SLOT;
+    if (wanted && !wait_warp(s->full[nb % Ti::NS], (nb / Ti::NS) & 1, s, p.status)) return;
     if (nv < kL) {  // rows behind the last position may hold anything: 0 x anything has to be 0
-      if (!wait_warp(s->full[nc % Ti::NS], (nc / Ti::NS) & 1, s, p.status)) return false;
-      if (wanted && j >= nv)
-        for (int u = u0; u < u0 + UN; ++u) *reinterpret_cast<uint4 *>(src + sw128(j, u)) = make_uint4(0u, 0u, 0u, 0u);
+      if (!wait_warp(s->full[nc % Ti::NS], (nc / Ti::NS) & 1, s, p.status)) return;
       uint8_t *tc = sm + Ti::RING + nc % Ti::NS * Ti::SLOT;
+      if (j >= nv) {
 #pragma unroll 1
-      for (int e = t; e < (int)(Ti::CT / 16); e += kKeyThreads)
-        if (((e >> 3) & 127) >= nv) reinterpret_cast<uint4 *>(tc)[e] = make_uint4(0u, 0u, 0u, 0u);
+        for (int u = 0; u < 8; ++u) {
+          for (uint32_t o = 0; o < Ti::BT && wanted; o += kHalf) *reinterpret_cast<uint4 *>(src + o + sw128(j, u)) = make_uint4(0u, 0u, 0u, 0u);
+          for (uint32_t o = 0; o < Ti::CT; o += kHalf) *reinterpret_cast<uint4 *>(tc + o + sw128(j, u)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
       fence_proxy_async_smem();
       arrive_warp(s->c_clean);
     }
-    if (!wanted) return true;
-    const int64_t n = p.reverse ? j + 1 + (OUT ? 0 : ch.start(it) - ch.t0)
-                                : (OUT ? nv : ch.t1 - ch.start(it)) - 1 - j;
+    if (!wanted) return;
+    const int n = p.reverse ? j + 1 + (OUT ? 0 : ch.start(it) - ch.t0) : (OUT ? nv : ch.t1 - ch.start(it)) - 1 - j;
     const float w = j < nv ? p.sk * power(g2, n) : 0.f;
     // the weight in two bfloat16 parts; fma rounds once
     const uint32_t w1 = pack2(w, w), w2 = pack2(w - lo16(w1), w - lo16(w1));
-    if (terms == 1) return convert(src, [&](uint32_t x) { return fmab(w1, x, mulb(w2, x)); });
-    // second term, negated: what the rounding of the first leaves is exact
-    const uint32_t m1 = w1 ^ 0x80008000u, m2 = w2 ^ 0x80008000u;
-    return convert(src, [&](uint32_t x) { return mulb(w1, x); }) &&
-           convert(src, [&](uint32_t x) { return fmab(m2, x, fmab(m1, x, mulb(w1, x))); });
-  };
-  const int w = (t >> 5) & 3, lane = t & 31, i = 32 * w + lane, half = t >> 7;
+    if (terms == 1) {
+      if (!convert(src, [&](uint32_t x) { return fmab(w1, x, mulb(w2, x)); })) return;
+    } else {
+      // second term, negated: what the rounding of the first leaves is exact
+      const uint32_t m1 = w1 ^ 0x80008000u, m2 = w2 ^ 0x80008000u;
+      if (!convert(src, [&](uint32_t x) { return mulb(w1, x); }) ||
+          !convert(src, [&](uint32_t x) { return fmab(m2, x, fmab(m1, x, mulb(w1, x))); }))
+        return;
+    }
+  }
+}
+
+// P warpgroups: the masked, weighted scores, rounded to bfloat16, in tensor
+// memory over the scores' own columns; a thread has a row and half its columns,
+// and the halves' P lies at columns 0 and 64.
+__device__ __forceinline__ void scores_role(const Pass &p, Bars *s, const Chunks &ch, float g2) {
+  const int t = threadIdx.x & 255, w = (t >> 5) & 3, lane = t & 31, half = t >> 7;
   const uint32_t tm = s->tmem + ((uint32_t)(32 * w) << 16) + 64 * half;
   const float f = p.si * p.sk;
   const bool moderate = g2 * 31.f > -100.f;
+  const uint32_t causal = p.reverse ? ~0u << lane : (2u << lane) - 1u;  // columns of the diagonal block that count
   const float *tab = p.reverse ? s->up : s->down;
-  auto scores = [&](int it) {
+#pragma unroll 1
+  for (int it = 0; it < ch.n; ++it) {
     const int nv = ch.valid(it);
-    if (!wait_warp(s->scores, it & 1, s, p.status)) return false;
+    if (!wait_warp(s->scores, it & 1, s, p.status)) return;
     tc_after_sync();
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k) {  // 16 columns from c0 on
-      const int c0 = 64 * half + 16 * k, cb = c0 >> 5;
+    for (int k = 0; k < 4; ++k) {  // 16 columns from c0 on, of the block cb of 32
+      const int c0 = 64 * half + 16 * k, cb = c0 >> 5, q0 = c0 & 16;
       uint32_t out[8];
       if (p.reverse ? cb < w || c0 >= nv : cb > w) {
 #pragma unroll
@@ -452,24 +468,27 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
       } else {
         uint32_t v[16];
         tmem_ld16_nowait(tm + 16 * k, v);
-        // lam^{|i-j|} as a factor of the row and one of the column (by blocks
-        // of 32 columns); on the diagonal the row's is up to lam^{-31}, so
-        // strong decays take the product from a table there
-        const bool diag = cb == w;
-        const f2 e = both(f * ex2(g2 * (float)(p.reverse ? 32 * cb - i : i - 32 * cb - 31)));
-        const int q0 = c0 & 16;
+        uint32_t keep = (cb == w ? causal : ~0u) >> q0;
+        if (c0 + 16 > nv) keep &= nv > c0 ? (1u << (nv - c0)) - 1u : 0u;  // columns behind the last position may hold anything
+        // lam^{|i-j|} as a factor of the row and one of the column; on the
+        // diagonal the row's is up to lam^{-31}, so strong decays take the
+        // product from a table there
+        const int i = 32 * (w - cb) + lane;
+        const f2 e = both(f * ex2(g2 * (float)(p.reverse ? -i : i - 31)));
         tmem_wait_ld();
         pin(v);
-        if (nv - c0 < 16) {  // columns behind the last position may hold anything
 #pragma unroll
-          for (int r = 0; r < 16; ++r) v[r] = c0 + r < nv ? v[r] : 0u;
-        }
-        if (diag && !moderate) {
+        for (int r = 0; r < 16; ++r) v[r] = (keep >> r) & 1u ? v[r] : 0u;
+        if (cb == w && !moderate) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {  // twice 8 columns, to stay short
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const int n0 = p.reverse ? q0 + 2 * r - lane : lane - 2 * r - q0, n1 = p.reverse ? n0 + 1 : n0 - 1;
-            out[r] = pack2(n0 >= 0 ? __uint_as_float(v[2 * r]) * (f * s->up[n0 & 31]) : 0.f,
-                           n1 >= 0 ? __uint_as_float(v[2 * r + 1]) * (f * s->up[n1 & 31]) : 0.f);
+            for (int r = 0; r < 4; ++r) {
+              const int n0 = p.reverse ? q0 + 8 * h + 2 * r - lane : lane - 2 * r - 8 * h - q0, n1 = p.reverse ? n0 + 1 : n0 - 1;
+              const float x0 = __uint_as_float(h ? v[2 * r + 8] : v[2 * r]), x1 = __uint_as_float(h ? v[2 * r + 9] : v[2 * r + 1]);
+              const uint32_t o = pack2(x0 * (n0 >= 0 ? f * s->up[n0 & 31] : 0.f), x1 * (n1 >= 0 ? f * s->up[n1 & 31] : 0.f));
+              if (h) out[r + 4] = o; else out[r] = o;
+            }
           }
         } else {
 #pragma unroll
@@ -478,16 +497,6 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
             out[2 * q] = pack2(mul2(pair_at(v + 4 * q), mul2(e, z.x)));
             out[2 * q + 1] = pack2(mul2(pair_at(v + 4 * q + 2), mul2(e, z.y)));
           }
-          if (diag) {
-            // pairs (2 r, 2 r + 1) against the row: kept, half kept, dropped;
-            // columns kept, from the last (first) on
-            const int d = p.reverse ? 16 + q0 - lane : lane + 1 - q0;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const int m = d - (p.reverse ? 14 - 2 * r : 2 * r);
-              out[r] = m >= 2 ? out[r] : m == 1 ? out[r] & (p.reverse ? 0xFFFF0000u : 0xFFFFu) : 0u;
-            }
-          }
         }
       }
       tmem_st8(tm + 8 * k, out);
@@ -495,14 +504,6 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
     tmem_wait_st();
     tc_before_sync();
     arrive_warp(s->p_ready);
-    return true;
-  };
-#pragma unroll 1
-  for (int it = -1; it < ch.n; ++it) {
-    if (it >= 0) {
-      if (OUT && !scores(it)) return;
-    }
-    if (it + 1 < ch.n && !keys(it + 1)) return;
   }
 }
 
@@ -516,7 +517,7 @@ __device__ __forceinline__ void output_role(const Pass &p, Bars *s, const Chunks
   for (int it = 0; it < ch.n; ++it) {
     const int nv = ch.valid(it);
     const f2 w = both(i < nv ? p.si * power(g2, p.reverse ? nv - 1 - i : i + 1) : 0.f);
-    const int64_t t = ch.start(it) + i;
+    const int64_t t = (int64_t)ch.start(it) + i;
     uint16_t *dst = static_cast<uint16_t *>(const_cast<void *>(p.o.p)) + b * p.o.sb + h * p.o.sh + t * p.o.st;
     if (!wait_warp(s->o_done, it & 1, s, p.status)) return;
     tc_after_sync();
@@ -559,7 +560,7 @@ __device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, c
   using Ti = Tiles<XP, YP, OUT>;
   int n = 0;  // tiles whose loads were issued
   for (int it = 0; it < ch.n; ++it) {
-    const int t = (int)ch.start(it);
+    const int t = ch.start(it);
     bool ok = true;
     for (int k = 0; k < Ti::PER; ++k) {
       const int slot = n % Ti::NS;
@@ -602,7 +603,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
       if (!(ok = loaded(nb) && loaded(na))) break;
       if (elect_one()) {
         const uint64_t da = kmajor(ta), db = kmajor(tb);
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < XP / 16; ++k) mma_ss(tm + SCORES, da + kstep(k), db + kstep(k), idesc(128, 128, false, false), k > 0);
         mma_commit(smem_addr(&s->scores));
       }
@@ -622,7 +623,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
           const uint64_t dw = mnmajor(sm + Ti::W + buf * Ti::BT, kHalf), dc = mnmajor(tc, kHalf);
           const bool acc = OUT || it > 0 || k > 0;
           const uint32_t id = idesc(128, YP, true, true) | (k > 0 ? kNegateA : 0u);
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < kL / 16; ++i)
             mma_ss(tm + ST, dw + mnstep(i), dc + mnstep(i), id, acc || i > 0);
           mma_commit(smem_addr(&s->w_free[buf]));
@@ -635,7 +636,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
         tc_after_sync();
         if (elect_one()) {
           const uint64_t da = kmajor(ta), dr = mnmajor(sm + Ti::R, XP * 128);
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < XP / 16; ++i)
             mma_ss(tm + O2, da + kstep(i), dr + mnstep(i), idesc(128, YP, false, true), i > 0);
           mma_commit(smem_addr(&s->empty[na % Ti::NS]));
@@ -658,7 +659,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
     if (elect_one()) {
       if (OUT) {
         const uint64_t dc = mnmajor(tc, kHalf);
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < kL / 16; ++k)
           mma_ts(tm + O1, tm + SCORES + 8 * k + (k >= 4 ? 32 : 0), dc + mnstep(k), idesc(128, YP, false, true), k > 0);
         mma_commit(smem_addr(&s->o_done));
@@ -677,6 +678,22 @@ struct Maps {
   CUtensorMap a[3], b[3], c[3];
   int terms[3], wide[3];
 };
+// Zeros in the chunks without valid positions.  (The block's place is read
+// anew: nothing of this stays in registers while the roles run.)
+__device__ __forceinline__ void zero_padding(const Group &group) {
+  uint32_t block;
+  asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(block));
+  const Pass &p = group.p[block % (unsigned)group.n];
+  const int64_t unit = block / (unsigned)group.n, bh = unit / p.nseg, t0 = unit % p.nseg * p.seg_len, b = bh / p.H;
+  const int64_t tz = min(t0 + p.seg_len, p.T), t1 = max(t0, min(tz, row_len(p, b)));
+  const int64_t z0 = min(t0 + (t1 - t0 + kL - 1) / kL * kL, tz);
+  const int units = p.Y / 8;
+  uint16_t *dst = static_cast<uint16_t *>(const_cast<void *>(p.o.p)) + b * p.o.sb + bh % p.H * p.o.sh;
+#pragma unroll 1
+  for (int64_t e = threadIdx.x; e < (tz - z0) * units; e += blockDim.x)
+    reinterpret_cast<uint4 *>(dst + (z0 + e / units) * p.o.st)[e % units] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // A block is a segment of a head of one pass; the passes of a segment are
 // neighbours, so that those that read the same tensors find them in L2.
 template <int XP, int YP, bool OUT>
@@ -695,11 +712,10 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
   uint8_t *sm = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
   const int64_t n = row_len(p, b);
   Chunks ch;
-  ch.t0 = sg * p.seg_len;
-  const int64_t tz = min(ch.t0 + p.seg_len, p.T);
-  ch.t1 = max(ch.t0, min(tz, n));
-  ch.c0 = ch.t0 / kL;
-  ch.n = (int)((ch.t1 - ch.t0 + kL - 1) / kL);
+  const int64_t t0 = sg * p.seg_len, tz = min(t0 + p.seg_len, p.T);  // segments are whole chunks
+  ch.t0 = (int)t0;
+  ch.t1 = (int)max(t0, min(tz, n));
+  ch.n = (ch.t1 - ch.t0 + kL - 1) / kL;
   ch.reverse = p.reverse;
   const float g = p.log_decay[h], g2 = g * kLog2e;
   const int warp = __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0);
@@ -707,7 +723,8 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
     for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 1);
     for (uint64_t *f : {&bars.scores, &bars.w_free[0], &bars.w_free[1], &bars.state, &bars.o_done, &bars.drain})
       mbar_init(smem_addr(f), 1);
-    for (uint64_t *f : {&bars.w_full[0], &bars.w_full[1], &bars.c_clean, &bars.p_ready}) mbar_init(smem_addr(f), kKeyThreads / 32);
+    for (uint64_t *f : {&bars.w_full[0], &bars.w_full[1], &bars.c_clean}) mbar_init(smem_addr(f), kKeyThreads / 32);
+    mbar_init(smem_addr(&bars.p_ready), kScoreWarps);
     for (uint64_t *f : {&bars.o_free, &bars.r_ready}) mbar_init(smem_addr(f), 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -722,8 +739,10 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
   tc_after_sync();
   if (warp < 4) {
     state_role<XP, YP, OUT>(p, &bars, sm, ch, unit, g);
-  } else if (OUT && warp < Ro::KEYS) {
+  } else if (OUT && warp < 8) {
     output_role<YP>(p, &bars, ch, b, h, g2, wide != 0);
+  } else if (OUT && warp < Ro::KEYS) {
+    scores_role(p, &bars, ch, g2);
   } else if (warp < Ro::LOAD) {
     keys_role<XP, YP, OUT>(p, &bars, sm, ch, terms, g2);
   } else {
@@ -731,14 +750,7 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
     else mma_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, terms);
   }
   __syncwarp();
-  if (OUT) {  // chunks without valid positions
-    const int units = p.Y / 8;
-    const int64_t z0 = min((ch.c0 + ch.n) * (int64_t)kL, tz);
-    for (int64_t e = threadIdx.x; e < (tz - z0) * units; e += blockDim.x) {
-      uint16_t *dst = static_cast<uint16_t *>(const_cast<void *>(p.o.p)) + b * p.o.sb + h * p.o.sh;
-      reinterpret_cast<uint4 *>(dst + (z0 + e / units) * p.o.st)[e % units] = make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
+  if (OUT) zero_padding(group);
   tc_before_sync();
   __syncthreads();
   if (warp == 0) {
