@@ -117,6 +117,26 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
 #pragma unroll
   for (int k = 0; k < N; ++k) asm volatile("" : "+r"(r[k]));
 }
+// f(c, v) for c = first, first + 1, .. end - 1 and the 16 columns v from
+// tm + 16 c on: one set is on its way while f has the other.
+template <typename F>
+__device__ __forceinline__ void tmem_each16(uint32_t tm, int first, int end, F f) {
+  uint32_t v[16], u[16];
+  if (first < end) tmem_ld16_nowait(tm + 16 * first, v);
+#pragma unroll 1
+  for (int c = first; c < end; c += 2) {
+    tmem_wait_ld();
+    pin(v);
+    if (c + 1 < end) tmem_ld16_nowait(tm + 16 * (c + 1), u);
+    f(c, v);
+    if (c + 1 < end) {
+      tmem_wait_ld();
+      pin(u);
+      if (c + 2 < end) tmem_ld16_nowait(tm + 16 * (c + 2), v);
+      f(c + 1, u);
+    }
+  }
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -126,6 +146,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -326,27 +354,22 @@ __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, 
         const Decay d = decay_of(g, ch.valid(it));
         const f2 dm = both(d.m);
         tc_after_sync();
-#pragma unroll 1
-        for (int yb = 0; yb < YP; yb += 32) {
-          uint32_t v[32];
-          tmem_ld32_nowait(tm + yb, v);
-          tmem_wait_ld();
-          pin(v);
-          uint8_t *half = sm + Ti::R + (yb >> 6) * (XP * 128);
+        tmem_each16(tm, 0, YP / 16, [&](int c, uint32_t(&v)[16]) {
+              uint8_t *half = sm + Ti::R + (c >> 2) * (XP * 128);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t *f = v + 8 * u;
-            *reinterpret_cast<uint4 *>(half + sw128(x, ((yb & 63) >> 3) + u)) =
-                make_uint4(pack2(pair_at(f)), pack2(pair_at(f + 2)), pack2(pair_at(f + 4)), pack2(pair_at(f + 6)));
+              for (int u = 0; u < 2; ++u) {
+                uint32_t *f = v + 8 * u;
+                *reinterpret_cast<uint4 *>(half + sw128(x, 2 * (c & 3) + u)) =
+                    make_uint4(pack2(pair_at(f)), pack2(pair_at(f + 2)), pack2(pair_at(f + 4)), pack2(pair_at(f + 6)));
 #pragma unroll
-            for (int q = 0; q < 8; q += 2) {  // decayed(), by pairs
-              const f2 z = pair_at(f + q);
-              const float2 r = unpair(fma2(z, dm, d.near_one ? z : 0ull));
-              f[q] = __float_as_uint(r.x), f[q + 1] = __float_as_uint(r.y);
-            }
-          }
-          tmem_st32(tm + yb, v);
-        }
+                for (int q = 0; q < 8; q += 2) {  // decayed(), by pairs
+                  const f2 z = pair_at(f + q);
+                  const float2 r = unpair(fma2(z, dm, d.near_one ? z : 0ull));
+                  f[q] = __float_as_uint(r.x), f[q + 1] = __float_as_uint(r.y);
+                }
+              }
+              tmem_st16(tm + 16 * c, v);
+            });
         tmem_wait_st();
         tc_before_sync();
         fence_proxy_async_smem();
@@ -458,48 +481,43 @@ __device__ __forceinline__ void scores_role(const Pass &p, Bars *s, const Chunks
     const int nv = ch.valid(it);
     if (!wait_warp(s->scores, it & 1, s, p.status)) return;
     tc_after_sync();
-#pragma unroll 1
-    for (int k = 0; k < 4; ++k) {  // 16 columns from c0 on, of the block cb of 32
-      const int c0 = 64 * half + 16 * k, cb = c0 >> 5, q0 = c0 & 16;
-      uint32_t out[8];
-      if (p.reverse ? cb < w || c0 >= nv : cb > w) {
+    // 16 columns at a time, k = k0 .. k1 - 1 of the half's 4; P is zero in the
+    // others (written last: its columns are those of scores)
+    const int k0 = p.reverse ? min(max(2 * (w - 2 * half), 0), 4) : 0;
+    const int k1 = p.reverse ? max(min(4, (nv - 64 * half + 15) >> 4), k0) : min(max(2 * (w - 2 * half + 1), 0), 4);
+    tmem_each16(tm, k0, k1, [&](int k, uint32_t(&v)[16]) {
+          const int c0 = 64 * half + 16 * k, cb = c0 >> 5, q0 = c0 & 16;  // from column c0 on, of the block cb of 32
+          uint32_t out[8];
+          uint32_t keep = (cb == w ? causal : ~0u) >> q0;
+          if (c0 + 16 > nv) keep &= nv > c0 ? (1u << (nv - c0)) - 1u : 0u;  // what lies behind the last position may be anything
+          // lam^{|i-j|} as a factor of the row and one of the column; on the
+          // diagonal the row's is up to lam^{-31}, so strong decays take the
+          // product from a table there
+          const int i = 32 * (w - cb) + lane;
+          const f2 e = both(f * ex2(g2 * (float)(p.reverse ? -i : i - 31)));
 #pragma unroll
-        for (int r = 0; r < 8; ++r) out[r] = 0u;
-      } else {
-        uint32_t v[16];
-        tmem_ld16_nowait(tm + 16 * k, v);
-        uint32_t keep = (cb == w ? causal : ~0u) >> q0;
-        if (c0 + 16 > nv) keep &= nv > c0 ? (1u << (nv - c0)) - 1u : 0u;  // columns behind the last position may hold anything
-        // lam^{|i-j|} as a factor of the row and one of the column; on the
-        // diagonal the row's is up to lam^{-31}, so strong decays take the
-        // product from a table there
-        const int i = 32 * (w - cb) + lane;
-        const f2 e = both(f * ex2(g2 * (float)(p.reverse ? -i : i - 31)));
-        tmem_wait_ld();
-        pin(v);
+          for (int r = 0; r < 16; ++r) v[r] = (keep >> r) & 1u ? v[r] : 0u;
+          if (cb == w && !moderate) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = (keep >> r) & 1u ? v[r] : 0u;
-        if (cb == w && !moderate) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {  // twice 8 columns, to stay short
+            for (int r = 0; r < 8; ++r) {
+              const int n0 = p.reverse ? q0 + 2 * r - lane : lane - 2 * r - q0, n1 = p.reverse ? n0 + 1 : n0 - 1;
+              out[r] = pack2(__uint_as_float(v[2 * r]) * (f * s->up[max(n0, 0)]),
+                             __uint_as_float(v[2 * r + 1]) * (f * s->up[max(n1, 0)]));
+            }
+          } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int n0 = p.reverse ? q0 + 8 * h + 2 * r - lane : lane - 2 * r - 8 * h - q0, n1 = p.reverse ? n0 + 1 : n0 - 1;
-              const float x0 = __uint_as_float(h ? v[2 * r + 8] : v[2 * r]), x1 = __uint_as_float(h ? v[2 * r + 9] : v[2 * r + 1]);
-              const uint32_t o = pack2(x0 * (n0 >= 0 ? f * s->up[n0 & 31] : 0.f), x1 * (n1 >= 0 ? f * s->up[n1 & 31] : 0.f));
-              if (h) out[r + 4] = o; else out[r] = o;
+            for (int q = 0; q < 4; ++q) {
+              const ulonglong2 z = *reinterpret_cast<const ulonglong2 *>(tab + q0 + 4 * q);
+              out[2 * q] = pack2(mul2(pair_at(v + 4 * q), mul2(e, z.x)));
+              out[2 * q + 1] = pack2(mul2(pair_at(v + 4 * q + 2), mul2(e, z.y)));
             }
           }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const ulonglong2 z = *reinterpret_cast<const ulonglong2 *>(tab + q0 + 4 * q);
-            out[2 * q] = pack2(mul2(pair_at(v + 4 * q), mul2(e, z.x)));
-            out[2 * q + 1] = pack2(mul2(pair_at(v + 4 * q + 2), mul2(e, z.y)));
-          }
-        }
-      }
-      tmem_st8(tm + 8 * k, out);
+          tmem_st8(tm + 8 * k, out);
+        });
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t zero[8] = {};
+      if (k < k0 || k >= k1) tmem_st8(tm + 8 * k, zero);
     }
     tmem_wait_st();
     tc_before_sync();
@@ -521,22 +539,25 @@ __device__ __forceinline__ void output_role(const Pass &p, Bars *s, const Chunks
     uint16_t *dst = static_cast<uint16_t *>(const_cast<void *>(p.o.p)) + b * p.o.sb + h * p.o.sh + t * p.o.st;
     if (!wait_warp(s->o_done, it & 1, s, p.status)) return;
     tc_after_sync();
+    uint32_t o1[16], o2[16], z[8];
+    tmem_ld16_nowait(tm, o1);
+    tmem_ld16_nowait(tm + YP, o2);
 #pragma unroll 1
     for (int y = 0; y < YP; y += 16) {
-      uint32_t o1[16], o2[16], z[8];
-      tmem_ld16_nowait(tm + y, o1);
-      tmem_ld16_nowait(tm + YP + y, o2);
       tmem_wait_ld();
       pin(o1);
       pin(o2);
-      if (y == YP - 16) {
-        tc_before_sync();
-        arrive_warp(s->o_free);
-      }
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         z[r] = pack2(fma2(w, pair_at(o2 + 2 * r), pair_at(o1 + 2 * r)));
         if (i >= nv) z[r] = 0u;
+      }
+      if (y < YP - 16) {
+        tmem_ld16_nowait(tm + y + 16, o1);
+        tmem_ld16_nowait(tm + YP + y + 16, o2);
+      } else {
+        tc_before_sync();
+        arrive_warp(s->o_free);
       }
       if (t < p.T && wide) {
         if (y < p.Y)
