@@ -51,6 +51,7 @@ namespace decay {
 constexpr int kL = 128;                  // positions per chunk
 constexpr uint32_t kHalf = kL * 128;     // bytes of 128 rows of 64 bfloat16
 constexpr uint32_t kTmemCols = 512;
+constexpr int kMostSlots = 8;             // of the ring of tiles
 constexpr uint32_t kTries = 1u << 23;    // bound on any one wait
 
 // ------------------------------------------------------------ tcgen05 ---
@@ -219,25 +220,30 @@ __device__ __forceinline__ f2 pair_at(const uint32_t *r) { return pair(__uint_as
 __device__ __forceinline__ float power(float g2, int n) { return n == 0 ? 1.f : ex2(g2 * (float)n); }
 
 // ------------------------------------------------------------- the pass ---
-// Shared memory: two buffers for the terms of the weighted keys, a ring of NS
-// tiles that the chunks' a, b and c pass through in this order, and the
-// state's bfloat16 copy.  With four slots each tile's load is issued half a
-// chunk's time or more before its first use.  With X = 64 the state's products run with
-// M = 128: their rows from 64 on are the bytes behind the term (there always
-// are some) and their results are not read.
+// Shared memory: a buffer for each term of the weighted keys, a ring of tiles
+// that the chunks' b, a and c pass through in this order, and the state's
+// bfloat16 copy.  The order decides which tile waits for which slot: with four
+// slots a waits for the b of the chunk before it (free once its scores and keys
+// are done), c for that chunk's a, b for the c of the one before.  With X = 64
+// the state's products run with M = 128: their rows from 64 on are the bytes
+// behind the term (there always are some) and their results are not read.
 template <int XP, int YP, bool OUT>
 struct Tiles {
   static constexpr uint32_t BT = XP / 64 * kHalf, CT = YP / 64 * kHalf, RT = OUT ? YP / 64 * XP * 128 : 0;
   static constexpr uint32_t SLOT = BT > CT ? BT : CT;
   static constexpr uint32_t MOST = 224 * 1024;
-  static constexpr int NS = (int)((MOST - 2 * BT - RT) / SLOT) < 8 ? (int)((MOST - 2 * BT - RT) / SLOT) : 8;
-  static constexpr int PER = OUT ? 3 : 2;  // tiles of a chunk: (a,) b, c
-  static constexpr uint32_t W = 0, RING = 2 * BT, R = RING + NS * SLOT, BYTES = R + RT;
-  static_assert(NS >= 4 && BYTES <= MOST, "the tiles, their alignment and the barriers fit 227 KB");
+  static constexpr int slots(int terms) {
+    const int n = (int)((MOST - terms * BT - RT) / SLOT);
+    return n < kMostSlots ? n : kMostSlots;
+  }
+  static constexpr int PER = OUT ? 3 : 2;  // tiles of a chunk: b, (a,) c
+  static constexpr uint32_t R = 0, W = RT;
+  static constexpr uint32_t BYTES = MOST;
+  static_assert(slots(2) >= 4, "the ring holds a chunk and more");
 };
 
 struct Bars {
-  uint64_t full[8], empty[8];  // ring slots
+  uint64_t full[kMostSlots], empty[kMostSlots];  // ring slots
   uint64_t scores;             // a b^T complete (MMA)
   uint64_t p_ready;            // P in tensor memory (P warpgroups)
   uint64_t w_full[2];          // a term of the weighted keys in its buffer (key warpgroup)
@@ -292,6 +298,15 @@ __device__ __forceinline__ void arrive_warp(uint64_t &bar) {
       "r"(threadIdx.x & 31u)
       : "memory");
 }
+
+// A place in the ring of `ns` tiles.
+struct Place {
+  int slot;
+  uint32_t phase;
+  __device__ __forceinline__ Place next(int ns) const { return slot == ns - 1 ? Place{0, phase ^ 1u} : Place{slot + 1, phase}; }
+};
+template <typename Ti>
+__device__ __forceinline__ uint32_t ring(int terms) { return Ti::W + terms * Ti::BT; }
 
 // The chunks of this CTA's segment, in the pass's order.
 struct Chunks {
@@ -406,11 +421,14 @@ template <int XP, int YP, bool OUT>
 __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int terms, float g2) {
   using Ti = Tiles<XP, YP, OUT>;
   const int j = threadIdx.x - 32 * Roles<OUT>::KEYS;
+  const int ns = Ti::slots(terms);
+  Place place{0, 0};
   int term = 0;  // terms so far
   // One term of a chunk: f of every pair of the tile at src.
   auto convert = [&](uint8_t *src, auto f) {
-    const int buf = term & 1;
-    if (term >= 2 && !wait_warp(s->w_free[buf], ((term >> 1) - 1) & 1, s, p.status)) return false;
+    // one buffer: term's use of it is number `term`, two: number term / 2
+    const int buf = terms == 1 ? 0 : term & 1, use = terms == 1 ? term : term >> 1;
+    if (use > 0 && !wait_warp(s->w_free[buf], (use - 1) & 1, s, p.status)) return false;
     uint8_t *dst = sm + Ti::W + buf * Ti::BT;
 #pragma unroll 1
     for (uint32_t o = 0; o < Ti::BT; o += kHalf) {
@@ -432,13 +450,14 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
 #pragma unroll 1
   for (int it = 0; it < ch.n; ++it) {
     const int nv = ch.valid(it);
-    const int nc = Ti::PER * it + Ti::PER - 1, nb = nc - 1;
+    const Place b = place, c = OUT ? b.next(ns).next(ns) : b.next(ns);
+    place = c.next(ns);
     const bool wanted = wants_state<OUT>(p) || it + 1 < ch.n;
-    uint8_t *src = sm + Ti::RING + nb % Ti::NS * Ti::SLOT;
-    if (wanted && !wait_warp(s->full[nb % Ti::NS], (nb / Ti::NS) & 1, s, p.status)) return;
+    uint8_t *src = sm + ring<Ti>(terms) + b.slot * Ti::SLOT;
+    if (wanted && !wait_warp(s->full[b.slot], b.phase, s, p.status)) return;
     if (nv < kL) {  // rows behind the last position may hold anything: 0 x anything has to be 0
-      if (!wait_warp(s->full[nc % Ti::NS], (nc / Ti::NS) & 1, s, p.status)) return;
-      uint8_t *tc = sm + Ti::RING + nc % Ti::NS * Ti::SLOT;
+      if (!wait_warp(s->full[c.slot], c.phase, s, p.status)) return;
+      uint8_t *tc = sm + ring<Ti>(terms) + c.slot * Ti::SLOT;
       if (j >= nv) {
 #pragma unroll 1
         for (int u = 0; u < 8; ++u) {
@@ -576,32 +595,36 @@ __device__ __forceinline__ void output_role(const Pass &p, Bars *s, const Chunks
 // Loads: the tiles of each chunk in the ring's order, each as soon as its slot
 // is free; one whole warp.
 template <int XP, int YP, bool OUT>
-__device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, int b, int h,
-                                          const CUtensorMap *am, const CUtensorMap *bm, const CUtensorMap *cm) {
+__device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, int terms, int b,
+                                          int h, const CUtensorMap *am, const CUtensorMap *bm, const CUtensorMap *cm) {
   using Ti = Tiles<XP, YP, OUT>;
+  const int ns = Ti::slots(terms);
+  Place place{0, 0};
   int n = 0;  // tiles whose loads were issued
-  for (int it = 0; it < ch.n; ++it) {
+  bool ok = true;
+#pragma unroll 1
+  for (int it = 0; it < ch.n && ok; ++it) {
     const int t = ch.start(it);
-    bool ok = true;
+#pragma unroll 1
     for (int k = 0; k < Ti::PER; ++k) {
-      const int slot = n % Ti::NS;
-      if (n >= Ti::NS && !(ok = wait_warp(s->empty[slot], (n / Ti::NS - 1) & 1, s, p.status))) break;
+      const int slot = place.slot;
+      if (n >= ns && !(ok = wait_warp(s->empty[slot], place.phase ^ 1u, s, p.status))) break;
       const bool is_c = k == Ti::PER - 1;
-      const CUtensorMap *m = is_c ? cm : k == Ti::PER - 2 ? bm : am;
-      const uint32_t bytes = is_c ? Ti::CT : Ti::BT, dst = sm + Ti::RING + slot * Ti::SLOT, bar = smem_addr(&s->full[slot]);
+      const CUtensorMap *m = is_c ? cm : k == 0 ? bm : am;
+      const uint32_t bytes = is_c ? Ti::CT : Ti::BT, dst = sm + ring<Ti>(terms) + slot * Ti::SLOT,
+                     bar = smem_addr(&s->full[slot]);
       if (elect_one()) {
         mbar_expect_tx(bar, bytes);
         for (uint32_t o = 0; o < bytes; o += kHalf) tma_load_4d(dst + o, m, (int)(o / kHalf) * 64, t, h, b, bar);
       }
       __syncwarp();
       ++n;
+      place = place.next(ns);
     }
-    if (!ok) break;
   }
   // The loads in flight write shared memory that outlives this warp, not the
   // CTA: every one is waited for (in order to end; consumers wait for theirs).
-  if (elect_one())
-    for (int k = max(0, n - Ti::NS); k < n; ++k) spin(smem_addr(&s->full[k % Ti::NS]), (k / Ti::NS) & 1);
+  for (int k = max(0, n - ns); k < n; ++k) spin(smem_addr(&s->full[k % ns]), (k / ns) & 1);
 }
 
 // MMAs, in the order that the head of this file explains; one whole warp.
@@ -610,14 +633,17 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
   using Ti = Tiles<XP, YP, OUT>;
   constexpr uint32_t SCORES = 0, O1 = 128, O2 = 128 + YP, ST = 128 + 2 * YP;
   const uint32_t tm = __shfl_sync(~0u, s->tmem, 0);
-  auto loaded = [&](int n) { return wait_warp(s->full[n % Ti::NS], (n / Ti::NS) & 1, s, p.status); };
-  auto tile = [&](int n) { return sm + Ti::RING + n % Ti::NS * Ti::SLOT; };
+  const int ns = Ti::slots(terms);
+  auto loaded = [&](const Place &t) { return wait_warp(s->full[t.slot], t.phase, s, p.status); };
+  auto tile = [&](const Place &t) { return sm + ring<Ti>(terms) + t.slot * Ti::SLOT; };
+  Place place{0, 0};
   int term = 0;  // terms of the keys so far
   bool ok = true;
 #pragma unroll 1
   for (int it = 0; it < ch.n; ++it) {
     const uint32_t ph = it & 1;
-    const int na = Ti::PER * it, nc = na + Ti::PER - 1, nb = nc - 1;
+    const Place nb = place, na = OUT ? nb.next(ns) : nb, nc = na.next(ns);
+    place = nc.next(ns);
     const uint32_t ta = tile(na), tb = tile(nb), tc = tile(nc);
     const int n_terms = wants_state<OUT>(p) || it + 1 < ch.n ? terms : 0;
     if (OUT) {
@@ -637,8 +663,8 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
 #pragma unroll 1
     for (int k = 0; k < max(n_terms, 1); ++k) {
       if (n_terms > 0) {
-        const int buf = term & 1;
-        if (!(ok = wait_warp(s->w_full[buf], (term >> 1) & 1, s, p.status))) break;
+        const int buf = terms == 1 ? 0 : term & 1, use = terms == 1 ? term : term >> 1;
+        if (!(ok = wait_warp(s->w_full[buf], use & 1, s, p.status))) break;
         tc_after_sync();
         if (elect_one()) {
           const uint64_t dw = mnmajor(sm + Ti::W + buf * Ti::BT, kHalf), dc = mnmajor(tc, kHalf);
@@ -660,17 +686,17 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
 #pragma unroll 4
           for (int i = 0; i < XP / 16; ++i)
             mma_ss(tm + O2, da + kstep(i), dr + mnstep(i), idesc(128, YP, false, true), i > 0);
-          mma_commit(smem_addr(&s->empty[na % Ti::NS]));
+          mma_commit(smem_addr(&s->empty[na.slot]));
         }
         __syncwarp();
       }
     }
     if (!ok) break;
+    // b is free once its keys (waited for above) and its scores are formed
+    if (OUT && !(ok = wait_warp(s->scores, ph, s, p.status))) break;
     if (elect_one()) {
+      mbar_arrive(smem_addr(&s->empty[nb.slot]));
       if (n_terms > 0 && (OUT || it + 1 == ch.n)) mma_commit(smem_addr(&s->state));
-      // the last term's arrival said that b was read, too
-      if (OUT) mma_commit(smem_addr(&s->empty[nb % Ti::NS]));
-      else mbar_arrive(smem_addr(&s->empty[nb % Ti::NS]));
     }
     __syncwarp();
     if (OUT) {
@@ -685,7 +711,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
           mma_ts(tm + O1, tm + SCORES + 8 * k + (k >= 4 ? 32 : 0), dc + mnstep(k), idesc(128, YP, false, true), k > 0);
         mma_commit(smem_addr(&s->o_done));
       }
-      mma_commit(smem_addr(&s->empty[nc % Ti::NS]));
+      mma_commit(smem_addr(&s->empty[nc.slot]));
     }
     __syncwarp();
   }
@@ -741,7 +767,7 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
   const float g = p.log_decay[h], g2 = g * kLog2e;
   const int warp = __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 1);
+    for (int i = 0; i < kMostSlots; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 1);
     for (uint64_t *f : {&bars.scores, &bars.w_free[0], &bars.w_free[1], &bars.state, &bars.o_done, &bars.drain})
       mbar_init(smem_addr(f), 1);
     for (uint64_t *f : {&bars.w_full[0], &bars.w_full[1], &bars.c_clean}) mbar_init(smem_addr(f), kKeyThreads / 32);
@@ -767,7 +793,7 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
   } else if (warp < Ro::LOAD) {
     keys_role<XP, YP, OUT>(p, &bars, sm, ch, terms, g2);
   } else {
-    if (warp == Ro::LOAD) load_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, (int)b, (int)h, &am, &bm, &cm);
+    if (warp == Ro::LOAD) load_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, terms, (int)b, (int)h, &am, &bm, &cm);
     else mma_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, terms);
   }
   __syncwarp();
