@@ -64,19 +64,23 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
 }
 __device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// D (tensor memory) = A B (+ D if `acc`): A from shared memory, or from tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// Upper word of every shared-memory matrix descriptor here: 1024 bytes between
+// groups of 8 rows, 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+// D (tensor memory) = A B (+ D if `acc`): A from shared memory, or from tensor
+// memory.  a and b are descriptors' lower words (below).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh)
       : "memory");
 }
 // One lane of a converged warp.  The MMA and load warps run their loops whole
@@ -165,16 +169,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 
 // Shared-memory matrix descriptors of tiles in the 128-byte swizzle: rows of
 // 64 bfloat16 (128 bytes), wider tiles as consecutive halves of `rows` rows.
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
+// The upper word is the same for all (1024 bytes between groups of 8 rows);
+// the lower one holds the address and the distance between halves, and a step
+// along the contraction adds to it (addresses below 256 KB do not carry out).
+__device__ __forceinline__ uint32_t sdesc(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
 // Contraction along the rows' 64-wide halves (128 rows); the step to the
-// 16-wide slice k16 (addresses below 256 KB do not carry out of their field).
-__device__ __forceinline__ uint64_t kmajor(uint32_t tile) { return sdesc(tile, 16u, 1024u); }
+// 16-wide slice k16.
+__device__ __forceinline__ uint32_t kmajor(uint32_t tile) { return sdesc(tile, 16u); }
 __device__ __forceinline__ constexpr uint32_t kstep(int k16) { return (kHalf * (k16 >> 2) + 32u * (k16 & 3)) >> 4; }
 // Contraction down the rows; `half` bytes between 64-wide groups of columns.
-__device__ __forceinline__ uint64_t mnmajor(uint32_t tile, uint32_t half) { return sdesc(tile, half, 1024u); }
+__device__ __forceinline__ uint32_t mnmajor(uint32_t tile, uint32_t half) { return sdesc(tile, half); }
 __device__ __forceinline__ constexpr uint32_t mnstep(int k16) { return 2048u * k16 >> 4; }
 // Instruction descriptor: bf16 x bf16 -> f32, M x N, operand majors, A negated.
 constexpr uint32_t kNegateA = 1u << 13;
@@ -649,8 +653,8 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
     if (OUT) {
       if (!(ok = loaded(nb) && loaded(na))) break;
       if (elect_one()) {
-        const uint64_t da = kmajor(ta), db = kmajor(tb);
-#pragma unroll 4
+        const uint32_t da = kmajor(ta), db = kmajor(tb);
+#pragma unroll
         for (int k = 0; k < XP / 16; ++k) mma_ss(tm + SCORES, da + kstep(k), db + kstep(k), idesc(128, 128, false, false), k > 0);
         mma_commit(smem_addr(&s->scores));
       }
@@ -667,10 +671,10 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
         if (!(ok = wait_warp(s->w_full[buf], use & 1, s, p.status))) break;
         tc_after_sync();
         if (elect_one()) {
-          const uint64_t dw = mnmajor(sm + Ti::W + buf * Ti::BT, kHalf), dc = mnmajor(tc, kHalf);
+          const uint32_t dw = mnmajor(sm + Ti::W + buf * Ti::BT, kHalf), dc = mnmajor(tc, kHalf);
           const bool acc = OUT || it > 0 || k > 0;
           const uint32_t id = idesc(128, YP, true, true) | (k > 0 ? kNegateA : 0u);
-#pragma unroll 4
+#pragma unroll
           for (int i = 0; i < kL / 16; ++i)
             mma_ss(tm + ST, dw + mnstep(i), dc + mnstep(i), id, acc || i > 0);
           mma_commit(smem_addr(&s->w_free[buf]));
@@ -682,8 +686,8 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
         if (it > 0 && !(ok = wait_warp(s->o_free, ph ^ 1u, s, p.status))) break;
         tc_after_sync();
         if (elect_one()) {
-          const uint64_t da = kmajor(ta), dr = mnmajor(sm + Ti::R, XP * 128);
-#pragma unroll 4
+          const uint32_t da = kmajor(ta), dr = mnmajor(sm + Ti::R, XP * 128);
+#pragma unroll
           for (int i = 0; i < XP / 16; ++i)
             mma_ss(tm + O2, da + kstep(i), dr + mnstep(i), idesc(128, YP, false, true), i > 0);
           mma_commit(smem_addr(&s->empty[na.slot]));
@@ -705,8 +709,8 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
     }
     if (elect_one()) {
       if (OUT) {
-        const uint64_t dc = mnmajor(tc, kHalf);
-#pragma unroll 4
+        const uint32_t dc = mnmajor(tc, kHalf);
+#pragma unroll
         for (int k = 0; k < kL / 16; ++k)
           mma_ts(tm + O1, tm + SCORES + 8 * k + (k >= 4 ? 32 : 0), dc + mnstep(k), idesc(128, YP, false, true), k > 0);
         mma_commit(smem_addr(&s->o_done));
@@ -760,8 +764,9 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
   const int64_t n = row_len(p, b);
   Chunks ch;
   const int64_t t0 = sg * p.seg_len, tz = min(t0 + p.seg_len, p.T);  // segments are whole chunks
+  // (through a shuffle: the compiler then knows that the loops are the same in all lanes)
   ch.t0 = (int)t0;
-  ch.t1 = (int)max(t0, min(tz, n));
+  ch.t1 = __shfl_sync(~0u, (int)max(t0, min(tz, n)), 0);
   ch.n = (ch.t1 - ch.t0 + kL - 1) / kL;
   ch.reverse = p.reverse;
   const float g = p.log_decay[h], g2 = g * kLog2e;
