@@ -224,34 +224,31 @@ __device__ __forceinline__ f2 pair_at(const uint32_t *r) { return pair(__uint_as
 __device__ __forceinline__ float power(float g2, int n) { return n == 0 ? 1.f : ex2(g2 * (float)n); }
 
 // ------------------------------------------------------------- the pass ---
-// Shared memory: a buffer for each term of the weighted keys, a ring of tiles
-// that the chunks' b, a and c pass through in this order, and the state's
-// bfloat16 copy.  The order decides which tile waits for which slot: with four
-// slots a waits for the b of the chunk before it (free once its scores and keys
-// are done), c for that chunk's a, b for the c of the one before.  With X = 64
-// the state's products run with M = 128: their rows from 64 on are the bytes
-// behind the term (there always are some) and their results are not read.
+// Shared memory: the state's bfloat16 copy, a buffer for the weighted keys (a
+// second term takes b's place), and a ring of tiles that the chunks' a, b and c
+// pass through in this order.  The order decides which tile waits for which
+// slot: with five slots c waits for the a of the chunk before it, a and b for b
+// and c of the one before that.  With X = 64 the state's products run with
+// M = 128: their rows from 64 on are the bytes behind the keys (there always
+// are some) and their results are not read.
 template <int XP, int YP, bool OUT>
 struct Tiles {
   static constexpr uint32_t BT = XP / 64 * kHalf, CT = YP / 64 * kHalf, RT = OUT ? YP / 64 * XP * 128 : 0;
   static constexpr uint32_t SLOT = BT > CT ? BT : CT;
   static constexpr uint32_t MOST = 224 * 1024;
-  static constexpr int slots(int terms) {
-    const int n = (int)((MOST - terms * BT - RT) / SLOT);
-    return n < kMostSlots ? n : kMostSlots;
-  }
-  static constexpr int PER = OUT ? 3 : 2;  // tiles of a chunk: b, (a,) c
-  static constexpr uint32_t R = 0, W = RT;
-  static constexpr uint32_t BYTES = MOST;
-  static_assert(slots(2) >= 4, "the ring holds a chunk and more");
+  static constexpr int FIT = (int)((MOST - BT - RT) / SLOT), NS = FIT < kMostSlots ? FIT : kMostSlots;
+  static constexpr int PER = OUT ? 3 : 2;  // tiles of a chunk: (a,) b, c
+  static constexpr uint32_t R = 0, W = RT, RING = W + BT, BYTES = RING + NS * SLOT;
+  static_assert(NS >= 5 && BYTES <= MOST, "the ring holds a chunk and more; the rows behind a b of the last slot exist");
+  static_assert(XP == 128 || SLOT > BT || BYTES + BT <= MOST, "");
 };
 
 struct Bars {
   uint64_t full[kMostSlots], empty[kMostSlots];  // ring slots
   uint64_t scores;             // a b^T complete (MMA)
   uint64_t p_ready;            // P in tensor memory (P warpgroups)
-  uint64_t w_full[2];          // a term of the weighted keys in its buffer (key warpgroup)
-  uint64_t w_free[2];          // its products complete (MMA)
+  uint64_t w_full[2];          // first and second term of the weighted keys in place (key warpgroup)
+  uint64_t w_free;             // the first term's products complete (MMA)
   uint64_t c_clean;            // c's rows behind the last position zeroed (key warpgroup; a segment has one such chunk)
   uint64_t state;              // a R and all products into the state complete (MMA)
   uint64_t r_ready;            // the state's copy in shared memory, the state decayed in tensor memory (state warpgroup)
@@ -303,14 +300,13 @@ __device__ __forceinline__ void arrive_warp(uint64_t &bar) {
       : "memory");
 }
 
-// A place in the ring of `ns` tiles.
+// A place in the ring of NS tiles.
+template <int NS>
 struct Place {
-  int slot;
-  uint32_t phase;
-  __device__ __forceinline__ Place next(int ns) const { return slot == ns - 1 ? Place{0, phase ^ 1u} : Place{slot + 1, phase}; }
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ Place next() const { return slot == NS - 1 ? Place{0, phase ^ 1u} : Place{slot + 1, phase}; }
 };
-template <typename Ti>
-__device__ __forceinline__ uint32_t ring(int terms) { return Ti::W + terms * Ti::BT; }
 
 // The chunks of this CTA's segment, in the pass's order.
 struct Chunks {
@@ -419,21 +415,15 @@ __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, 
   }
 }
 
-// Key warpgroup: lam^n b, as one bfloat16 term or two that pass through two
-// buffers; a thread has a row (position).
+// Key warpgroup: lam^n b, as one bfloat16 term or two, the second in b's place
+// once its scores are formed; a thread has a row (position).
 template <int XP, int YP, bool OUT>
 __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int terms, float g2) {
   using Ti = Tiles<XP, YP, OUT>;
   const int j = threadIdx.x - 32 * Roles<OUT>::KEYS;
-  const int ns = Ti::slots(terms);
-  Place place{0, 0};
-  int term = 0;  // terms so far
-  // One term of a chunk: f of every pair of the tile at src.
-  auto convert = [&](uint8_t *src, auto f) {
-    // one buffer: term's use of it is number `term`, two: number term / 2
-    const int buf = terms == 1 ? 0 : term & 1, use = terms == 1 ? term : term >> 1;
-    if (use > 0 && !wait_warp(s->w_free[buf], (use - 1) & 1, s, p.status)) return false;
-    uint8_t *dst = sm + Ti::W + buf * Ti::BT;
+  Place<Ti::NS> place;
+  // One term: f of every pair of the tile at src.
+  auto convert = [&](const uint8_t *src, uint8_t *dst, uint64_t &full, auto f) {
 #pragma unroll 1
     for (uint32_t o = 0; o < Ti::BT; o += kHalf) {
 #pragma unroll
@@ -447,21 +437,19 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
       }
     }
     fence_proxy_async_smem();
-    arrive_warp(s->w_full[buf]);
-    ++term;
-    return true;
+    arrive_warp(full);
   };
 #pragma unroll 1
   for (int it = 0; it < ch.n; ++it) {
     const int nv = ch.valid(it);
-    const Place b = place, c = OUT ? b.next(ns).next(ns) : b.next(ns);
-    place = c.next(ns);
+    const Place<Ti::NS> b = OUT ? place.next() : place, c = b.next();
+    place = c.next();
     const bool wanted = wants_state<OUT>(p) || it + 1 < ch.n;
-    uint8_t *src = sm + ring<Ti>(terms) + b.slot * Ti::SLOT;
+    uint8_t *src = sm + Ti::RING + b.slot * Ti::SLOT, *dst = sm + Ti::W;
     if (wanted && !wait_warp(s->full[b.slot], b.phase, s, p.status)) return;
     if (nv < kL) {  // rows behind the last position may hold anything: 0 x anything has to be 0
       if (!wait_warp(s->full[c.slot], c.phase, s, p.status)) return;
-      uint8_t *tc = sm + ring<Ti>(terms) + c.slot * Ti::SLOT;
+      uint8_t *tc = sm + Ti::RING + c.slot * Ti::SLOT;
       if (j >= nv) {
 #pragma unroll 1
         for (int u = 0; u < 8; ++u) {
@@ -477,14 +465,15 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
     const float w = j < nv ? p.sk * power(g2, n) : 0.f;
     // the weight in two bfloat16 parts; fma rounds once
     const uint32_t w1 = pack2(w, w), w2 = pack2(w - lo16(w1), w - lo16(w1));
+    if (it > 0 && !wait_warp(s->w_free, (it - 1) & 1, s, p.status)) return;
     if (terms == 1) {
-      if (!convert(src, [&](uint32_t x) { return fmab(w1, x, mulb(w2, x)); })) return;
+      convert(src, dst, s->w_full[0], [&](uint32_t x) { return fmab(w1, x, mulb(w2, x)); });
     } else {
+      convert(src, dst, s->w_full[0], [&](uint32_t x) { return mulb(w1, x); });
+      if (OUT && !wait_warp(s->scores, it & 1, s, p.status)) return;
       // second term, negated: what the rounding of the first leaves is exact
       const uint32_t m1 = w1 ^ 0x80008000u, m2 = w2 ^ 0x80008000u;
-      if (!convert(src, [&](uint32_t x) { return mulb(w1, x); }) ||
-          !convert(src, [&](uint32_t x) { return fmab(m2, x, fmab(m1, x, mulb(w1, x))); }))
-        return;
+      convert(src, src, s->w_full[1], [&](uint32_t x) { return fmab(m2, x, fmab(m1, x, mulb(w1, x))); });
     }
   }
 }
@@ -599,11 +588,10 @@ __device__ __forceinline__ void output_role(const Pass &p, Bars *s, const Chunks
 // Loads: the tiles of each chunk in the ring's order, each as soon as its slot
 // is free; one whole warp.
 template <int XP, int YP, bool OUT>
-__device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, int terms, int b,
-                                          int h, const CUtensorMap *am, const CUtensorMap *bm, const CUtensorMap *cm) {
+__device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, int b, int h,
+                                          const CUtensorMap *am, const CUtensorMap *bm, const CUtensorMap *cm) {
   using Ti = Tiles<XP, YP, OUT>;
-  const int ns = Ti::slots(terms);
-  Place place{0, 0};
+  Place<Ti::NS> place;
   int n = 0;  // tiles whose loads were issued
   bool ok = true;
 #pragma unroll 1
@@ -612,23 +600,22 @@ __device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, c
 #pragma unroll 1
     for (int k = 0; k < Ti::PER; ++k) {
       const int slot = place.slot;
-      if (n >= ns && !(ok = wait_warp(s->empty[slot], place.phase ^ 1u, s, p.status))) break;
+      if (n >= Ti::NS && !(ok = wait_warp(s->empty[slot], place.phase ^ 1u, s, p.status))) break;
       const bool is_c = k == Ti::PER - 1;
-      const CUtensorMap *m = is_c ? cm : k == 0 ? bm : am;
-      const uint32_t bytes = is_c ? Ti::CT : Ti::BT, dst = sm + ring<Ti>(terms) + slot * Ti::SLOT,
-                     bar = smem_addr(&s->full[slot]);
+      const CUtensorMap *m = is_c ? cm : k == Ti::PER - 2 ? bm : am;
+      const uint32_t bytes = is_c ? Ti::CT : Ti::BT, dst = sm + Ti::RING + slot * Ti::SLOT, bar = smem_addr(&s->full[slot]);
       if (elect_one()) {
         mbar_expect_tx(bar, bytes);
         for (uint32_t o = 0; o < bytes; o += kHalf) tma_load_4d(dst + o, m, (int)(o / kHalf) * 64, t, h, b, bar);
       }
       __syncwarp();
       ++n;
-      place = place.next(ns);
+      place = place.next();
     }
   }
   // The loads in flight write shared memory that outlives this warp, not the
   // CTA: every one is waited for (in order to end; consumers wait for theirs).
-  for (int k = max(0, n - ns); k < n; ++k) spin(smem_addr(&s->full[k % ns]), (k / ns) & 1);
+  for (int k = max(0, n - Ti::NS); k < n; ++k) spin(smem_addr(&s->full[k % Ti::NS]), (k / Ti::NS) & 1);
 }
 
 // MMAs, in the order that the head of this file explains; one whole warp.
@@ -637,21 +624,19 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
   using Ti = Tiles<XP, YP, OUT>;
   constexpr uint32_t SCORES = 0, O1 = 128, O2 = 128 + YP, ST = 128 + 2 * YP;
   const uint32_t tm = __shfl_sync(~0u, s->tmem, 0);
-  const int ns = Ti::slots(terms);
-  auto loaded = [&](const Place &t) { return wait_warp(s->full[t.slot], t.phase, s, p.status); };
-  auto tile = [&](const Place &t) { return sm + ring<Ti>(terms) + t.slot * Ti::SLOT; };
-  Place place{0, 0};
-  int term = 0;  // terms of the keys so far
+  auto loaded = [&](const Place<Ti::NS> &t) { return wait_warp(s->full[t.slot], t.phase, s, p.status); };
+  auto tile = [&](const Place<Ti::NS> &t) { return sm + Ti::RING + t.slot * Ti::SLOT; };
+  Place<Ti::NS> place;
   bool ok = true;
 #pragma unroll 1
   for (int it = 0; it < ch.n; ++it) {
     const uint32_t ph = it & 1;
-    const Place nb = place, na = OUT ? nb.next(ns) : nb, nc = na.next(ns);
-    place = nc.next(ns);
+    const Place<Ti::NS> na = place, nb = OUT ? na.next() : na, nc = nb.next();
+    place = nc.next();
     const uint32_t ta = tile(na), tb = tile(nb), tc = tile(nc);
     const int n_terms = wants_state<OUT>(p) || it + 1 < ch.n ? terms : 0;
     if (OUT) {
-      if (!(ok = loaded(nb) && loaded(na))) break;
+      if (!(ok = loaded(na) && loaded(nb))) break;
       if (elect_one()) {
         const uint32_t da = kmajor(ta), db = kmajor(tb);
 #pragma unroll
@@ -667,20 +652,18 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
 #pragma unroll 1
     for (int k = 0; k < max(n_terms, 1); ++k) {
       if (n_terms > 0) {
-        const int buf = terms == 1 ? 0 : term & 1, use = terms == 1 ? term : term >> 1;
-        if (!(ok = wait_warp(s->w_full[buf], use & 1, s, p.status))) break;
+        if (!(ok = wait_warp(s->w_full[k], ph, s, p.status))) break;
         tc_after_sync();
         if (elect_one()) {
-          const uint32_t dw = mnmajor(sm + Ti::W + buf * Ti::BT, kHalf), dc = mnmajor(tc, kHalf);
+          const uint32_t dw = mnmajor(k == 0 ? sm + Ti::W : tb, kHalf), dc = mnmajor(tc, kHalf);
           const bool acc = OUT || it > 0 || k > 0;
           const uint32_t id = idesc(128, YP, true, true) | (k > 0 ? kNegateA : 0u);
 #pragma unroll
           for (int i = 0; i < kL / 16; ++i)
             mma_ss(tm + ST, dw + mnstep(i), dc + mnstep(i), id, acc || i > 0);
-          mma_commit(smem_addr(&s->w_free[buf]));
+          if (k == 0) mma_commit(smem_addr(&s->w_free));
         }
         __syncwarp();
-        ++term;
       }
       if (OUT && k == 0) {
         if (it > 0 && !(ok = wait_warp(s->o_free, ph ^ 1u, s, p.status))) break;
@@ -696,10 +679,9 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
       }
     }
     if (!ok) break;
-    // b is free once its keys (waited for above) and its scores are formed
-    if (OUT && !(ok = wait_warp(s->scores, ph, s, p.status))) break;
     if (elect_one()) {
-      mbar_arrive(smem_addr(&s->empty[nb.slot]));
+      // b is free once its scores are formed and its keys read, or multiplied
+      mma_commit(smem_addr(&s->empty[nb.slot]));
       if (n_terms > 0 && (OUT || it + 1 == ch.n)) mma_commit(smem_addr(&s->state));
     }
     __syncwarp();
@@ -773,7 +755,7 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
   const int warp = __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMostSlots; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 1);
-    for (uint64_t *f : {&bars.scores, &bars.w_free[0], &bars.w_free[1], &bars.state, &bars.o_done, &bars.drain})
+    for (uint64_t *f : {&bars.scores, &bars.w_free, &bars.state, &bars.o_done, &bars.drain})
       mbar_init(smem_addr(f), 1);
     for (uint64_t *f : {&bars.w_full[0], &bars.w_full[1], &bars.c_clean}) mbar_init(smem_addr(f), kKeyThreads / 32);
     mbar_init(smem_addr(&bars.p_ready), kScoreWarps);
@@ -798,7 +780,7 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
   } else if (warp < Ro::LOAD) {
     keys_role<XP, YP, OUT>(p, &bars, sm, ch, terms, g2);
   } else {
-    if (warp == Ro::LOAD) load_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, terms, (int)b, (int)h, &am, &bm, &cm);
+    if (warp == Ro::LOAD) load_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, (int)b, (int)h, &am, &bm, &cm);
     else mma_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, terms);
   }
   __syncwarp();
@@ -856,7 +838,7 @@ cudaError_t launch_t(const Group &g, cudaStream_t st) {
   Maps m{};
   if (!encoder() || !ensure_context()) return cudaErrorNotSupported;
   const auto kern = decay_tc_kernel<XP, YP, OUT>;
-  constexpr int smem = (int)Tiles<XP, YP, OUT>::BYTES + 1024;
+  constexpr int smem = (int)Tiles<XP, YP, OUT>::MOST + 1024;
   int blocks = 0;
   const cudaError_t e = blocks_per_sm((const void *)kern, Roles<OUT>::THREADS, smem, &blocks);
   if (e != cudaSuccess) return e;
