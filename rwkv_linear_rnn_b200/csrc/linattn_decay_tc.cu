@@ -122,24 +122,16 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
 #pragma unroll
   for (int k = 0; k < N; ++k) asm volatile("" : "+r"(r[k]));
 }
-// f(c, v) for c = first, first + 1, .. end - 1 and the 16 columns v from
-// tm + 16 c on: one set is on its way while f has the other.
+// f(c, v) for c = first, first + 1, .. end - 1 and the 16 columns v from tm + 16 c on.
 template <typename F>
 __device__ __forceinline__ void tmem_each16(uint32_t tm, int first, int end, F f) {
-  uint32_t v[16], u[16];
-  if (first < end) tmem_ld16_nowait(tm + 16 * first, v);
 #pragma unroll 1
-  for (int c = first; c < end; c += 2) {
+  for (int c = first; c < end; ++c) {
+    uint32_t v[16];
+    tmem_ld16_nowait(tm + 16 * c, v);
     tmem_wait_ld();
     pin(v);
-    if (c + 1 < end) tmem_ld16_nowait(tm + 16 * (c + 1), u);
     f(c, v);
-    if (c + 1 < end) {
-      tmem_wait_ld();
-      pin(u);
-      if (c + 2 < end) tmem_ld16_nowait(tm + 16 * (c + 2), v);
-      f(c + 1, u);
-    }
   }
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -275,7 +267,8 @@ __device__ __forceinline__ bool spin(uint32_t addr, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
-      "TRY%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE%=;\n"
+      "TRY%=:\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE%=;\n"
       " add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra TRY%=;\n"
       "DONE%=:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
@@ -507,8 +500,10 @@ __device__ __forceinline__ void scores_role(const Pass &p, Bars *s, const Chunks
           // product from a table there
           const int i = 32 * (w - cb) + lane;
           const f2 e = both(f * ex2(g2 * (float)(p.reverse ? -i : i - 31)));
+          if (cb == w || c0 + 16 > nv) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) v[r] = (keep >> r) & 1u ? v[r] : 0u;
+            for (int r = 0; r < 16; ++r) v[r] = (keep >> r) & 1u ? v[r] : 0u;
+          }
           if (cb == w && !moderate) {
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
@@ -562,7 +557,10 @@ __device__ __forceinline__ void output_role(const Pass &p, Bars *s, const Chunks
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         z[r] = pack2(fma2(w, pair_at(o2 + 2 * r), pair_at(o1 + 2 * r)));
-        if (i >= nv) z[r] = 0u;
+      }
+      if (nv < kL) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) z[r] = i < nv ? z[r] : 0u;
       }
       if (y < YP - 16) {
         tmem_ld16_nowait(tm + y + 16, o1);
