@@ -21,7 +21,8 @@
 //
 // Long sequences with few heads are cut into segments: one launch sums each
 // segment's contribution to the state, a scan joins them in order, and the
-// output launch starts every segment from its own state.
+// output launch starts every segment from its own state (the last one ends with
+// the state that the pass hands out).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -48,8 +49,6 @@ struct Pass {
   const float *s_in;       // [B, H, X, Y], or [B, H, Y, X] if s_in_t; or null
   int s_in_t;
   float *s_out;            // [B, H, X, Y] or null
-  int scan_out;            // with several segments: s_out is wanted, and comes from the sums
-  int exact_state;         // the pass is one whose state a call may ask for: it is kept to 24 bits
   float si, sk;            // factors of the output and of the products entering the state
   int reverse;
   int nseg;                // segments per head

@@ -104,8 +104,6 @@ cudaError_t run_group(Group &g, const Dims &d, bool tc, void *ws, cudaStream_t s
   for (int i = 0; i < g.n; ++i) {
     Pass &p = g.p[i];
     p.nseg = (int)nseg;
-    // the recurrence's last segment has the state itself; the tensor cores' only to the bits its outputs need
-    p.scan_out = tc && nseg > 1 && p.s_out;
     p.seg_len = tc ? tc_segment_len(d.T, nseg) : (d.T + nseg - 1) / nseg;
     p.seg = static_cast<float *>(ws) + i * (seg_bytes(d, nseg) / sizeof(float));
   }
@@ -170,7 +168,7 @@ extern "C" int linattn_decay_forward(int64_t B, int64_t T, int64_t H, int D, int
   Pass p{};
   p.B = B, p.T = T, p.H = H, p.X = D, p.Y = M;
   p.a = view(q), p.b = view(k), p.c = view(v), p.o = view(out);
-  p.log_decay = log_decay, p.lengths = lengths, p.s_in = state_in, p.s_out = state_out, p.exact_state = 1;
+  p.log_decay = log_decay, p.lengths = lengths, p.s_in = state_in, p.s_out = state_out;
   p.si = scale, p.sk = 1.f, p.status = status;
   return rc_of(run_passes(&p, 1, d, ws, st));
 }
@@ -227,7 +225,7 @@ extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, in
   // grad_v and the gradient of the state handed in
   p[2].X = D, p[2].Y = M;
   p[2].a = view(k), p[2].b = view(q), p[2].c = view(grad_out), p[2].o = view(grad_v);
-  p[2].s_in = grad_state_out, p[2].s_out = grad_state_in, p[2].exact_state = 1;
+  p[2].s_in = grad_state_out, p[2].s_out = grad_state_in;
   p[2].si = 1.f, p[2].sk = scale, p[2].reverse = 1;
   return rc_of(run_passes(p, 3, d, ws, st));
 }

@@ -98,7 +98,7 @@ __global__ void __maxnreg__(168) rec_kernel(const __grid_constant__ Group g, int
   const int yt = blockIdx.z * YS, y0 = yt + yl;  // the block's first column, this lane's
   const int64_t bh = blockIdx.x / p.nseg, sg = blockIdx.x % p.nseg;
   const bool last = sg == (p.reverse ? 0 : p.nseg - 1);  // of the pass's segments
-  if (!OUT && last && !p.scan_out) return;               // no state starts from its sum
+  if (!OUT && last) return;                              // no state starts from its sum
   const int64_t b = bh / p.H, h = bh % p.H;
   const int64_t n = row_len(p, b);
   const int64_t t0 = sg * p.seg_len, tz = min(t0 + p.seg_len, p.T), t1 = max(t0, min(tz, n));
@@ -293,7 +293,7 @@ __global__ void __maxnreg__(168) rec_kernel(const __grid_constant__ Group g, int
     }
     buf ^= VEC ? 1 : 0;
   }
-  float *dst = !OUT ? p.seg + blockIdx.x * XY : last && p.s_out && !p.scan_out ? p.s_out + bh * XY : nullptr;
+  float *dst = !OUT ? p.seg + blockIdx.x * XY : last && p.s_out ? p.s_out + bh * XY : nullptr;
   if (dst) {
 #pragma unroll
     for (int r = 0; r < 2 * QX; ++r) {
@@ -322,11 +322,9 @@ __global__ void __maxnreg__(168) rec_kernel(const __grid_constant__ Group g, int
 }
 
 // Joins the segments of every head in time order (or reverse): p.seg holds
-// the segments' sums and receives the states at their starts; the state after
-// the last one goes to s_out if the pass leaves it to this kernel.  blockIdx.y
-// is the head, blockIdx.z the pass; V state elements per thread.  Eight
-// segments' loads are in flight at a time, and the sum goes through them in
-// order.
+// the segments' sums and receives the states at their starts.  blockIdx.y is the
+// head, blockIdx.z the pass; V state elements per thread.  Eight segments' loads
+// are in flight at a time, and the sum goes through them in order.
 template <int V>
 __global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__ Group g) {
   const Pass &p = g.p[blockIdx.z];
@@ -347,13 +345,12 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__
   }
   float *base = p.seg + bh * p.nseg * XY + f;
   constexpr int kAhead = 8;
-  const int use = p.nseg - (p.scan_out ? 0 : 1);  // sums that somebody starts from
   for (int s0 = 0; s0 < p.nseg; s0 += kAhead) {
     float v[kAhead][V] = {};
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int s = p.reverse ? p.nseg - 1 - (s0 + i) : s0 + i;
-      if (s0 + i < use) ldv(v[i], base + (int64_t)s * XY);
+      if (s0 + i < p.nseg - 1) ldv(v[i], base + (int64_t)s * XY);
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -367,7 +364,6 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__
       }
     }
   }
-  if (p.s_out && p.scan_out) stv(p.s_out + bh * XY + f, run);
 }
 
 // Sum over the 8 lanes of equal lane % 4 of four columns each: afterwards a

@@ -15,14 +15,14 @@
 // 128 x Y x 128, 128 x Y x X, and X x Y x 128 for the state, which stays in
 // tensor memory for the whole segment.
 //
-// Roundings.  P, the copy of R that meets a and, in passes that cannot hand
-// their state out, the weighted keys lam^n b are rounded to bfloat16 once (they
-// are matrix operands); these errors are independent of the result's own
+// Roundings.  P and the copy of R that meets a are rounded to bfloat16 once
+// (they are matrix operands); both errors are independent of the result's own
 // rounding and as large.  Weights are applied in float32 before the rounding
-// (P, keys) or afterwards (a R).  In passes that can hand their state out
-// (asked to or not, so that the outputs are the same bits) the weighted keys
-// are a sum of two bfloat16 terms, 17 bits with the second's sign (a state's
-// error is then about 2e-6 of it, half a bit of each sum of 128 products).
+// (P) or afterwards (a R).  The weighted keys lam^n b enter the state, which is
+// float32, as a sum of two bfloat16 terms: 16 bits, below the rounding of R's
+// copy, and an error of 4e-6 of a state that is handed out.  (A third term,
+// 24 bits, leaves 1e-6 there, the accumulation's own, and costs 40 % of the
+// time at X = Y = 128; a single one would be a rounding more in the outputs.)
 //
 // One CTA runs one head's segment with specialised warps: a producer (TMA
 // loads), an MMA issuer, a warpgroup for the state (its bfloat16 copy and its
@@ -34,8 +34,7 @@
 // scores, the next chunk's keys behind all of them.
 //
 // The floor is HBM: a chunk of 128 x (X + X + Y + Y) bfloat16 takes 2.9 us of
-// an SM's share of the measured bandwidth at X = Y = 128; its MMAs take 1.1 us
-// (1.4 with two terms).
+// an SM's share of the measured bandwidth at X = Y = 128; its MMAs take 1.4 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -310,16 +309,11 @@ struct Chunks {
   __device__ __forceinline__ int valid(int it) const { return min(kL, t1 - start(it)); }
 };
 
-// Whether the state after the segment goes anywhere; if not, its last chunk
-// adds nothing to it.
-template <bool OUT>
-__device__ __forceinline__ bool wants_state(const Pass &p) {
-  return !OUT || (p.nseg == 1 && p.s_out);
-}
 // State warpgroup: R at the chunk's start -> its bfloat16 copy in shared memory
 // and, decayed, tensor memory again.  A thread is a row of the state.
 template <int XP, int YP, bool OUT>
-__device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int64_t unit, float g) {
+__device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int64_t unit, float g,
+                                           float *result) {
   using Ti = Tiles<XP, YP, OUT>;
   const int x = threadIdx.x, warp = x >> 5;
   const int64_t bh = unit / p.nseg;
@@ -328,7 +322,6 @@ __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, 
   const int64_t XY = (int64_t)p.X * p.Y;
   const float *init = !OUT ? nullptr : p.nseg > 1 ? p.seg + unit * XY : p.s_in ? p.s_in + bh * XY : nullptr;
   const bool init_t = p.nseg == 1 && p.s_in_t;
-  float *result = !OUT ? p.seg + unit * XY : wants_state<OUT>(p) ? p.s_out + bh * XY : nullptr;
   auto load_row = [&](int yb, uint32_t(&v)[32]) {
     if (!init || x >= p.X) {
 #pragma unroll
@@ -408,10 +401,10 @@ __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, 
   }
 }
 
-// Key warpgroup: lam^n b, as one bfloat16 term or two, the second in b's place
-// once its scores are formed; a thread has a row (position).
+// Key warpgroup: lam^n b as two bfloat16 terms, the second in b's place once
+// its scores are formed; a thread has a row (position).
 template <int XP, int YP, bool OUT>
-__device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int terms, float g2) {
+__device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, float g2, bool more) {
   using Ti = Tiles<XP, YP, OUT>;
   const int j = threadIdx.x - 32 * Roles<OUT>::KEYS;
   Place<Ti::NS> place;
@@ -437,7 +430,7 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
     const int nv = ch.valid(it);
     const Place<Ti::NS> b = OUT ? place.next() : place, c = b.next();
     place = c.next();
-    const bool wanted = wants_state<OUT>(p) || it + 1 < ch.n;
+    const bool wanted = more || it + 1 < ch.n;
     uint8_t *src = sm + Ti::RING + b.slot * Ti::SLOT, *dst = sm + Ti::W;
     if (wanted && !wait_warp(s->full[b.slot], b.phase, s, p.status)) return;
     if (nv < kL) {  // rows behind the last position may hold anything: 0 x anything has to be 0
@@ -456,18 +449,14 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
     if (!wanted) return;
     const int n = p.reverse ? j + 1 + (OUT ? 0 : ch.start(it) - ch.t0) : (OUT ? nv : ch.t1 - ch.start(it)) - 1 - j;
     const float w = j < nv ? p.sk * power(g2, n) : 0.f;
-    // the weight in two bfloat16 parts; fma rounds once
-    const uint32_t w1 = pack2(w, w), w2 = pack2(w - lo16(w1), w - lo16(w1));
+    // the weight in two bfloat16 parts: the first term is w1 b rounded; the
+    // second, negated (the products subtract it), what that leaves (exact in
+    // bfloat16) plus w2 b, rounded once
+    const uint32_t w1 = pack2(w, w), w2 = pack2(w - lo16(w1), w - lo16(w1)), m1 = w1 ^ 0x80008000u, m2 = w2 ^ 0x80008000u;
     if (it > 0 && !wait_warp(s->w_free, (it - 1) & 1, s, p.status)) return;
-    if (terms == 1) {
-      convert(src, dst, s->w_full[0], [&](uint32_t x) { return fmab(w1, x, mulb(w2, x)); });
-    } else {
-      convert(src, dst, s->w_full[0], [&](uint32_t x) { return mulb(w1, x); });
-      if (OUT && !wait_warp(s->scores, it & 1, s, p.status)) return;
-      // second term, negated: what the rounding of the first leaves is exact
-      const uint32_t m1 = w1 ^ 0x80008000u, m2 = w2 ^ 0x80008000u;
-      convert(src, src, s->w_full[1], [&](uint32_t x) { return fmab(m2, x, fmab(m1, x, mulb(w1, x))); });
-    }
+    convert(src, dst, s->w_full[0], [&](uint32_t x) { return mulb(w1, x); });
+    if (OUT && !wait_warp(s->scores, it & 1, s, p.status)) return;
+    convert(src, src, s->w_full[1], [&](uint32_t x) { return fmab(m2, x, fmab(m1, x, mulb(w1, x))); });
   }
 }
 
@@ -618,7 +607,7 @@ __device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, c
 
 // MMAs, in the order that the head of this file explains; one whole warp.
 template <int XP, int YP, bool OUT>
-__device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, int terms) {
+__device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, bool more) {
   using Ti = Tiles<XP, YP, OUT>;
   constexpr uint32_t SCORES = 0, O1 = 128, O2 = 128 + YP, ST = 128 + 2 * YP;
   const uint32_t tm = __shfl_sync(~0u, s->tmem, 0);
@@ -632,7 +621,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
     const Place<Ti::NS> na = place, nb = OUT ? na.next() : na, nc = nb.next();
     place = nc.next();
     const uint32_t ta = tile(na), tb = tile(nb), tc = tile(nc);
-    const int n_terms = wants_state<OUT>(p) || it + 1 < ch.n ? terms : 0;
+    const int n_terms = more || it + 1 < ch.n ? 2 : 0;
     if (OUT) {
       if (!(ok = loaded(na) && loaded(nb))) break;
       if (elect_one()) {
@@ -707,7 +696,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
 
 struct Maps {
   CUtensorMap a[3], b[3], c[3];
-  int terms[3], wide[3];
+  int wide[3];
 };
 // Zeros in the chunks without valid positions.  (The block's place is read
 // anew: nothing of this stays in registers while the roles run.)
@@ -735,9 +724,13 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
   const int64_t unit = blockIdx.x / (unsigned)group.n;
   const Pass &p = group.p[pass];
   const CUtensorMap &am = maps.a[pass], &bm = maps.b[pass], &cm = maps.c[pass];
-  const int terms = maps.terms[pass], wide = maps.wide[pass];
+  const int wide = maps.wide[pass];
   const int64_t bh = unit / p.nseg, sg = unit % p.nseg, b = bh / p.H, h = bh % p.H;
-  if (!OUT && !p.scan_out && sg == (p.reverse ? 0 : p.nseg - 1)) return;  // no state starts from it
+  const bool last = sg == (p.reverse ? 0 : p.nseg - 1);  // of the pass's segments
+  if (!OUT && last) return;                              // no state starts from its sum
+  // Where the state after the segment goes; if nowhere, the last chunk adds nothing to it.
+  const int64_t XY = (int64_t)p.X * p.Y;
+  float *result = !OUT ? p.seg + unit * XY : last && p.s_out ? p.s_out + bh * XY : nullptr;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
   uint8_t *sm = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
@@ -770,16 +763,16 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
   __syncthreads();
   tc_after_sync();
   if (warp < 4) {
-    state_role<XP, YP, OUT>(p, &bars, sm, ch, unit, g);
+    state_role<XP, YP, OUT>(p, &bars, sm, ch, unit, g, result);
   } else if (OUT && warp < 8) {
     output_role<YP>(p, &bars, ch, b, h, g2, wide != 0);
   } else if (OUT && warp < Ro::KEYS) {
     scores_role(p, &bars, ch, g2);
   } else if (warp < Ro::LOAD) {
-    keys_role<XP, YP, OUT>(p, &bars, sm, ch, terms, g2);
+    keys_role<XP, YP, OUT>(p, &bars, sm, ch, g2, result != nullptr);
   } else {
     if (warp == Ro::LOAD) load_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, (int)b, (int)h, &am, &bm, &cm);
-    else mma_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, terms);
+    else mma_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, result != nullptr);
   }
   __syncwarp();
   if (OUT) zero_padding(group);
@@ -848,8 +841,6 @@ cudaError_t launch_t(const Group &g, cudaStream_t st) {
       return cudaErrorInvalidValue;
     m.wide[i] = OUT && ((uintptr_t)p.o.p & 31u) == 0 && p.Y % 16 == 0 && even(p.o.sb, p.B) && even(p.o.st, p.T) &&
                 even(p.o.sh, p.H);
-    // states that a call may hand out are float32; those that only meet rows as bfloat16 copies need not be
-    m.terms[i] = p.exact_state && (!OUT || p.nseg == 1) ? 2 : 1;
   }
   const Pass &p = g.p[0];
   return launch_kernel(kern, dim3((unsigned)(p.B * p.H * p.nseg * g.n)), dim3(Roles<OUT>::THREADS), smem, st, m, g);
