@@ -420,7 +420,7 @@ __device__ __forceinline__ void store_state(const float (&S)[RX][4], float *s, i
 // head, a warp 16 columns; each lane has its RX float4s of state in flight
 // before anything else.
 template <typename E, int RX>
-__global__ void __launch_bounds__(32 * kStepWarps) decay_step_kernel(StepArgs s) {
+__global__ void __launch_bounds__(32 * kStepWarps, 3) decay_step_kernel(StepArgs s) {
   constexpr int XP = 8 * RX;
   __shared__ float sq[XP], sk[XP], sv[16 * kStepWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -4,11 +4,11 @@
 // Pair i of a head at position p turns by the angle p inv_freq[i].  The
 // angle's turns are formed and reduced in float64 (p reaches 2^53 and float32
 // would lose whole radians from about 2^20 on), the remainder goes to
-// sincospi in float32.  A block takes a few positions and all their heads, so
-// each sine and cosine is computed once for q and k together (R / 2 of them
-// against (Hq + Hk) D elements read and written) and the kernel is bound by
-// HBM: every element is read once and written once, 16 bytes at a time when
-// the layout allows.
+// sincospi in float32.  Every element is read once and written once, 16 bytes
+// at a time when the layout allows: the kernel is bound by HBM.  A block has up
+// to 1024 items of one or a few positions, so that a sine and cosine serve all
+// heads of q and k; a thread's four items are on their way before the sines are
+// computed, and everything per item is 32-bit arithmetic without a division.
 #include <algorithm>
 #include <utility>
 
@@ -34,10 +34,15 @@ struct Args {
   const double *inv_freq;
   float mscale;
   int inverse;
-  int tokens;  // per block
+  int pairs, items;   // of a head: items that turn, all items
+  int tokens, parts;  // positions of a block, or blocks of a position's items
+  int share;          // items of such a block
+  uint32_t by_tok, by_head;  // for divisions by a position's and a head's items
 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kItems = 4;
+// e / d for e d < 2^32 with m = ceil(2^32 / d); 0 stands for d = 1.
+__device__ __forceinline__ uint32_t divide(uint32_t e, uint32_t m) { return m ? __umulhi(e, m) : e; }
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -47,118 +52,137 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return d;
 }
 
-// V elements of a tensor as float32: 16 bytes (VEC), or one.
+// V elements of a tensor: as they are stored (16 bytes, or one element), and as
+// float32.
 template <typename E, int V>
 struct Pack;
 template <>
 struct Pack<float, 4> {
-  static __device__ __forceinline__ void ld(const void *p, int64_t i, float (&x)[4]) {
-    const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  typedef uint4 Raw;
+  static __device__ __forceinline__ void get(const Raw &v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
-  static __device__ __forceinline__ void st(const void *p, int64_t i, const float (&x)[4]) {
-    *reinterpret_cast<float4 *>(static_cast<float *>(const_cast<void *>(p)) + i) = make_float4(x[0], x[1], x[2], x[3]);
+  static __device__ __forceinline__ Raw put(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
 };
 template <>
 struct Pack<uint16_t, 8> {
-  static __device__ __forceinline__ void ld(const void *p, int64_t i, float (&x)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+  typedef uint4 Raw;
+  static __device__ __forceinline__ void get(const Raw &v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[2 * k] = lo16(w[k]), x[2 * k + 1] = hi16(w[k]);
   }
-  static __device__ __forceinline__ void st(const void *p, int64_t i, const float (&x)[8]) {
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(const_cast<void *>(p)) + i) =
-        make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+  static __device__ __forceinline__ Raw put(const float (&x)[8]) {
+    return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
   }
 };
 template <>
 struct Pack<float, 1> {
-  static __device__ __forceinline__ void ld(const void *p, int64_t i, float (&x)[1]) {
-    x[0] = static_cast<const float *>(p)[i];
-  }
-  static __device__ __forceinline__ void st(const void *p, int64_t i, const float (&x)[1]) {
-    static_cast<float *>(const_cast<void *>(p))[i] = x[0];
-  }
+  typedef float Raw;
+  static __device__ __forceinline__ void get(const Raw &v, float (&x)[1]) { x[0] = v; }
+  static __device__ __forceinline__ Raw put(const float (&x)[1]) { return x[0]; }
 };
 template <>
 struct Pack<uint16_t, 1> {
-  static __device__ __forceinline__ void ld(const void *p, int64_t i, float (&x)[1]) {
-    x[0] = lo16(static_cast<const uint16_t *>(p)[i]);
-  }
-  static __device__ __forceinline__ void st(const void *p, int64_t i, const float (&x)[1]) {
-    static_cast<uint16_t *>(const_cast<void *>(p))[i] = (uint16_t)(pack2(x[0], 0.f) & 0xFFFFu);
-  }
+  typedef uint16_t Raw;
+  static __device__ __forceinline__ void get(const Raw &v, float (&x)[1]) { x[0] = lo16(v); }
+  static __device__ __forceinline__ Raw put(const float (&x)[1]) { return (uint16_t)(pack2(x[0], 0.f) & 0xFFFFu); }
 };
 
 // One item of a head: V pairs in the half layout (elements V j.. and
-// V j + R/2..); V/2 pairs in the interleaved one (2 V elements there when
-// V = 1); or, behind the pairs, V elements to copy.
+// V j + R/2..); V/2 pairs in the interleaved one (2 elements there when V = 1);
+// or, behind the pairs, V elements to copy.
 template <typename E, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(Args a) {
-  extern __shared__ float2 cs[];  // [tokens][R / 2]: cos, sin, times mscale
-  const int64_t all = a.B * a.T, first = (int64_t)blockIdx.x * a.tokens;
-  const int m = (int)min((int64_t)a.tokens, all - first);
-  const int half = a.R / 2;
-  for (int e = threadIdx.x; e < m * half; e += kThreads) {
-    const int64_t tok = first + e / half;
-    const int i = e % half;
-    const int64_t at = tok / a.T * a.pos_sb + tok % a.T;
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Args a) {
+  typedef Pack<E, V> P;
+  typedef typename P::Raw Raw;
+  constexpr bool TWO = !(INTER && V > 1);     // an item's pairs lie in two places
+  constexpr int W = INTER && V == 1 ? 2 : V;  // elements of an interleaved item
+  extern __shared__ float2 cs[];              // [tokens][R / 2]: cos, sin, times mscale
+  const uint32_t half = a.R / 2, per_tok = (uint32_t)(a.Hq + a.Hk) * a.items;
+  const uint32_t part = blockIdx.x % (uint32_t)a.parts;
+  const int64_t first = (int64_t)(blockIdx.x / (uint32_t)a.parts) * a.tokens, all = a.B * a.T;
+  const uint32_t m = (uint32_t)min((int64_t)a.tokens, all - first);
+  const uint32_t T = (uint32_t)a.T, b0 = (uint32_t)first / T, t0 = (uint32_t)first % T;
+  // items [from, to) of the block's m positions
+  const uint32_t from = part * a.share, to = a.parts > 1 ? min(from + a.share, per_tok) : m * per_tok;
+
+  Raw x[kItems][TWO ? 2 : 1];
+  E *dst[kItems];
+  uint32_t wi[kItems];  // the item's first entry of cs, or a mark
+  constexpr uint32_t kCopy = ~0u, kNone = ~1u;
+#pragma unroll
+  for (int n = 0; n < kItems; ++n) {
+    const uint32_t e = from + n * kThreads + threadIdx.x;
+    wi[n] = kNone;
+    if (e >= to) continue;
+    const uint32_t i = a.parts > 1 ? 0u : divide(e, a.by_tok), f = e - i * per_tok;
+    const uint32_t hh = V > 1 ? divide(f, a.by_head) : f / (uint32_t)a.items, j = f - hh * a.items;
+    uint32_t b = b0, t = t0 + i;
+    while (t >= T) t -= T, ++b;
+    const bool is_q = hh < (uint32_t)a.Hq;
+    const View &in = is_q ? a.q : a.k, &out = is_q ? a.oq : a.ok;
+    const uint32_t h = is_q ? hh : hh - a.Hq;
+    const E *src = static_cast<const E *>(in.p) + (b * in.sb + t * in.st + h * in.sh);
+    dst[n] = static_cast<E *>(const_cast<void *>(out.p)) + (b * out.sb + t * out.st + h * out.sh);
+    if (j < (uint32_t)a.pairs) {
+      const uint32_t x0 = INTER ? W * j : V * j;
+      wi[n] = i * half + (INTER ? x0 / 2 : x0);
+      x[n][0] = *reinterpret_cast<const Raw *>(src + x0);
+      if constexpr (TWO) x[n][1] = *reinterpret_cast<const Raw *>(src + (INTER ? x0 + 1 : x0 + half));
+      dst[n] += x0;
+    } else if (is_q ? a.copy_q : a.copy_k) {
+      const uint32_t x0 = a.R + V * (j - a.pairs);
+      wi[n] = kCopy;
+      x[n][0] = *reinterpret_cast<const Raw *>(src + x0);
+      dst[n] += x0;
+    }
+  }
+  for (uint32_t e = threadIdx.x; e < m * half; e += kThreads) {
+    const uint32_t i = e / half;
+    uint32_t b = b0, t = t0 + i;
+    while (t >= T) t -= T, ++b;
+    const int64_t at = b * a.pos_sb + t;
     const double p = a.pos64 ? (double)static_cast<const int64_t *>(a.pos)[at] : (double)static_cast<const int32_t *>(a.pos)[at];
-    const double turns = p * a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    const double turns = p * a.inv_freq[e - i * half] * 0.15915494309189533577;  // 1 / (2 pi)
     float sn, c;
     sincospif(2.f * (float)(turns - rint(turns)), &sn, &c);
     cs[e] = make_float2(a.mscale * c, a.inverse ? -a.mscale * sn : a.mscale * sn);
   }
   __syncthreads();
-  constexpr int W = INTER && V == 1 ? 2 : V;  // elements of an interleaved item
-  const int pairs = INTER ? a.R / W : half / V, tail = (a.D - a.R) / V;
-  const int items = pairs + (a.copy_q || a.copy_k ? tail : 0);
-  const int per_tok = (a.Hq + a.Hk) * items;
-  for (int e = threadIdx.x; e < m * per_tok; e += kThreads) {
-    const int i = e / per_tok, f = e % per_tok, hh = f / items, j = f % items;
-    const int64_t tok = first + i, b = tok / a.T, t = tok % a.T;
-    const bool is_q = hh < a.Hq;
-    const View &in = is_q ? a.q : a.k, &out = is_q ? a.oq : a.ok;
-    const int h = is_q ? hh : hh - a.Hq;
-    const int64_t src = b * in.sb + t * in.st + h * in.sh, dst = b * out.sb + t * out.st + h * out.sh;
-    if (j >= pairs) {
-      if (is_q ? a.copy_q : a.copy_k) {
-        const int64_t x = a.R + (int64_t)V * (j - pairs);
-        float v[V];
-        Pack<E, V>::ld(in.p, src + x, v);
-        Pack<E, V>::st(out.p, dst + x, v);
-      }
+#pragma unroll
+  for (int n = 0; n < kItems; ++n) {
+    if (wi[n] == kNone) continue;
+    if (wi[n] == kCopy) {
+      *reinterpret_cast<Raw *>(dst[n]) = x[n][0];
       continue;
     }
-    const float2 *w = cs + i * half;
-    if (INTER && V > 1) {
-      float v[V];
-      Pack<E, V>::ld(in.p, src + (int64_t)V * j, v);
+    const float2 *w = cs + wi[n];
+    float v[V];
+    P::get(x[n][0], v);
+    if constexpr (!TWO) {
 #pragma unroll
       for (int r = 0; r < V / 2; ++r) {
-        const float2 z = w[V / 2 * j + r];
-        const float x = v[2 * r], y = v[2 * r + 1];
-        v[2 * r] = x * z.x - y * z.y;
-        v[2 * r + 1] = x * z.y + y * z.x;
+        const float2 z = w[r];
+        const float p = v[2 * r], q = v[2 * r + 1];
+        v[2 * r] = p * z.x - q * z.y;
+        v[2 * r + 1] = p * z.y + q * z.x;
       }
-      Pack<E, V>::st(out.p, dst + (int64_t)V * j, v);
     } else {
-      const int64_t x0 = INTER ? 2 * (int64_t)j : (int64_t)V * j, x1 = INTER ? x0 + 1 : x0 + half;
-      float v[V], u[V];
-      Pack<E, V>::ld(in.p, src + x0, v);
-      Pack<E, V>::ld(in.p, src + x1, u);
+      float u[V];
+      P::get(x[n][1], u);
 #pragma unroll
       for (int r = 0; r < V; ++r) {
-        const float2 z = w[V * j + r];
-        const float x = v[r], y = u[r];
-        v[r] = x * z.x - y * z.y;
-        u[r] = x * z.y + y * z.x;
+        const float2 z = w[r];
+        const float p = v[r], q = u[r];
+        v[r] = p * z.x - q * z.y;
+        u[r] = p * z.y + q * z.x;
       }
-      Pack<E, V>::st(out.p, dst + x0, v);
-      Pack<E, V>::st(out.p, dst + x1, u);
+      *reinterpret_cast<Raw *>(dst[n] + (INTER ? 1 : half)) = P::put(u);
     }
+    *reinterpret_cast<Raw *>(dst[n]) = P::put(v);
   }
 }
 
@@ -169,15 +193,24 @@ namespace {
 using namespace wkv;
 using namespace wkv::rotary;
 
+uint32_t reciprocal(uint32_t d) { return d <= 1 ? 0u : 0xFFFFFFFFu / d + 1u; }
 template <typename E, int V>
 cudaError_t launch(Args a, bool inter, cudaStream_t st) {
-  // about 1024 items per block: enough loads in flight, and the sines shared
-  const int64_t items = std::max<int64_t>(1, (int64_t)(a.Hq + a.Hk) * (inter ? a.R / V : a.R / 2 / V));
-  a.tokens = (int)std::min<int64_t>(std::max<int64_t>(1, 1024 / items), 16);
-  const unsigned grid = (unsigned)((a.B * a.T + a.tokens - 1) / a.tokens);
-  const size_t smem = sizeof(float2) * a.tokens * (a.R / 2);
-  return inter ? launch_kernel(rotary_kernel<E, V, true>, dim3(grid), dim3(kThreads), smem, st, a)
-               : launch_kernel(rotary_kernel<E, V, false>, dim3(grid), dim3(kThreads), smem, st, a);
+  const int W = inter ? (V == 1 ? 2 : V) : V;
+  a.pairs = inter ? a.R / W : a.R / 2 / V;
+  a.items = a.pairs + (a.copy_q || a.copy_k ? (a.D - a.R) / V : 0);
+  const int64_t per_tok = (int64_t)(a.Hq + a.Hk) * a.items, most = kThreads * kItems, half = a.R / 2;
+  // few positions: fewer items each, over more blocks, to shorten the call
+  int64_t want = most;
+  while (want > kThreads && a.B * a.T * ((per_tok + want - 1) / want) < 592) want /= 2;
+  a.parts = (int)((per_tok + want - 1) / want);
+  a.share = (int)((per_tok + a.parts - 1) / a.parts);
+  a.tokens = a.parts > 1 ? 1 : (int)std::max<int64_t>(1, std::min({want / per_tok, int64_t(16), 4096 / half}));
+  a.by_tok = reciprocal((uint32_t)per_tok), a.by_head = reciprocal((uint32_t)a.items);
+  const int64_t blocks = (a.B * a.T + a.tokens - 1) / a.tokens * a.parts;
+  const size_t smem = sizeof(float2) * a.tokens * half;
+  return inter ? launch_kernel(rotary_kernel<E, V, true>, dim3((unsigned)blocks), dim3(kThreads), smem, st, a)
+               : launch_kernel(rotary_kernel<E, V, false>, dim3((unsigned)blocks), dim3(kThreads), smem, st, a);
 }
 
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
