@@ -83,18 +83,19 @@ constexpr float kSlowest = -16.f * 0.69314718f / kBatch;
 // the segment's start state; otherwise the segment's sum alone, from zero.
 // VEC: float32 in 16-byte pieces, fetched one batch ahead.  168 registers let
 // three warps share a scheduler.
-template <typename E, int TX, bool OUT, bool VEC>
-__global__ void __maxnreg__(168) rec_kernel(const __grid_constant__ Group g, int nx, int nwy) {
+template <typename E, int TX, int NX, bool OUT, bool VEC>
+__global__ void __maxnreg__(168) rec_kernel(const __grid_constant__ Group g, int nwy) {
   const Pass &p = g.p[blockIdx.y];
   extern __shared__ __align__(16) float rec_smem[];
   constexpr int QX = TX / 4;  // a lane's float4s of rows, 16 rows apart
-  const int XS = 4 * TX * nx, YS = 32 * nwy;
+  constexpr int XS = 4 * TX * NX;
+  const int YS = 32 * nwy;
   constexpr int NBUF = VEC ? 2 : 1;
   float *sb = rec_smem, *sc = sb + NBUF * kTB * XS, *sa = sc + NBUF * kTB * YS;  // sa, so: OUT only
-  float *so = sa + NBUF * kTB * XS;                                           // [nx][kTB][YS]
+  float *so = sa + NBUF * kTB * XS;                                           // [NX][kTB][YS]
   __shared__ __align__(16) float wk[kBatch], uk[kBatch];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wx = warp % nx;
-  const int rg = lane >> 3, x0 = 4 * TX * wx + 4 * rg, yl = 32 * (warp / nx) + 4 * (lane & 7);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wx = warp % NX;
+  const int rg = lane >> 3, x0 = 4 * TX * wx + 4 * rg, yl = 32 * (warp / NX) + 4 * (lane & 7);
   const int yt = blockIdx.z * YS, y0 = yt + yl;  // the block's first column, this lane's
   const int64_t bh = blockIdx.x / p.nseg, sg = blockIdx.x % p.nseg;
   const bool last = sg == (p.reverse ? 0 : p.nseg - 1);  // of the pass's segments
@@ -158,7 +159,8 @@ __global__ void __maxnreg__(168) rec_kernel(const __grid_constant__ Group g, int
 
   // rows s.. of the segment (m of them) into buffer `buf`.  A thread's pieces
   // of a and b are one column's, every rx-th row; of c every ry-th.
-  const int ux = XS / 4, uy = YS / 4, rx = blockDim.x / ux, ry = blockDim.x / uy;
+  constexpr int ux = XS / 4;
+  const int uy = YS / 4, rx = blockDim.x / ux, ry = blockDim.x / uy;
   const int ix = tid / ux, px = 4 * (tid % ux), iy = tid / uy, py = 4 * (tid % uy);
   auto fetch = [&](int64_t s, int m, int buf) {
     float *db = sb + buf * kTB * XS, *dc = sc + buf * kTB * YS, *da = sa + buf * kTB * XS;
@@ -278,7 +280,7 @@ __global__ void __maxnreg__(168) rec_kernel(const __grid_constant__ Group g, int
         if (yt + py < p.Y)
           for (int i = iy; i < m; i += ry, fo += jo, uo += 4 * blockDim.x) {
             float4 v = *reinterpret_cast<const float4 *>(uo);
-            if (nx == 2) {
+            if (NX == 2) {
               const float4 u = *reinterpret_cast<const float4 *>(uo + kTB * YS);
               v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
             }
@@ -287,7 +289,7 @@ __global__ void __maxnreg__(168) rec_kernel(const __grid_constant__ Group g, int
       } else {
         for (int e = tid; e < m * YS; e += blockDim.x) {
           const int i = e / YS, y = yt + e % YS;
-          if (y < p.Y) store1<E>(po, (t + step * i) * p.o.st + y, nx == 2 ? so[e] + so[kTB * YS + e] : so[e]);
+          if (y < p.Y) store1<E>(po, (t + step * i) * p.o.st + y, NX == 2 ? so[e] + so[kTB * YS + e] : so[e]);
         }
       }
     }
@@ -459,18 +461,16 @@ namespace {
 // Warps of 32 columns in a block; 128 columns are two blocks of two, so that
 // 12 warps fit an SM with two warps of rows as well.
 int rec_warps_y(int Y) { return Y > 96 ? 2 : (Y + 31) / 32; }
-template <typename E, int TX, bool VEC>
-cudaError_t rec_t(const Group &g, int nx, int nwy, int ytiles, bool sums_only, cudaStream_t st) {
+template <typename E, int TX, int NX, bool VEC>
+cudaError_t rec_t(const Group &g, int nwy, int ytiles, bool sums_only, cudaStream_t st) {
   const Pass &p = g.p[0];
-  const dim3 grid((unsigned)(p.B * p.H * p.nseg), (unsigned)g.n, (unsigned)ytiles), block(32 * nx * nwy);
-  const size_t rows = sizeof(float) * (VEC ? 2 : 1) * kTB * 4 * TX * nx, cols = sizeof(float) * kTB * 32 * nwy;
-  const size_t smem = sums_only ? rows + (VEC ? 2 : 1) * cols : 2 * rows + (VEC ? 2 : 1) * cols + nx * cols;
+  const dim3 grid((unsigned)(p.B * p.H * p.nseg), (unsigned)g.n, (unsigned)ytiles), block(32 * NX * nwy);
+  const size_t rows = sizeof(float) * (VEC ? 2 : 1) * kTB * 4 * TX * NX, cols = sizeof(float) * kTB * 32 * nwy;
+  const size_t smem = sums_only ? rows + (VEC ? 2 : 1) * cols : 2 * rows + (VEC ? 2 : 1) * cols + NX * cols;
+  const auto kern = sums_only ? rec_kernel<E, TX, NX, false, VEC> : rec_kernel<E, TX, NX, true, VEC>;
   int blocks = 0;  // raises the kernel's shared-memory limit
-  const void *kern = sums_only ? (const void *)rec_kernel<E, TX, false, VEC> : (const void *)rec_kernel<E, TX, true, VEC>;
-  const cudaError_t e = blocks_per_sm(kern, (int)block.x, (int)smem, &blocks);
-  if (e != cudaSuccess) return e;
-  return sums_only ? launch_kernel(rec_kernel<E, TX, false, VEC>, grid, block, smem, st, g, nx, nwy)
-                   : launch_kernel(rec_kernel<E, TX, true, VEC>, grid, block, smem, st, g, nx, nwy);
+  const cudaError_t e = blocks_per_sm((const void *)kern, (int)block.x, (int)smem, &blocks);
+  return e == cudaSuccess ? launch_kernel(kern, grid, block, smem, st, g, nwy) : e;
 }
 bool pieces16(const View &v, const Pass &p) {
   auto fits = [](int64_t s, int64_t n) { return n <= 1 || s % 4 == 0; };
@@ -481,7 +481,9 @@ cudaError_t rec_v(const Group &g, bool sums_only, cudaStream_t st) {
   int y = 0;
   for (int i = 0; i < g.n; ++i) y = std::max(y, g.p[i].Y);
   const int nwy = rec_warps_y(y), tiles = (y + 32 * nwy - 1) / (32 * nwy), cls = rec_class(g.p[0].X);
-  return cls == 0 ? rec_t<E, 8, VEC>(g, 1, nwy, tiles, sums_only, st) : rec_t<E, 16, VEC>(g, cls, nwy, tiles, sums_only, st);
+  return cls == 0   ? rec_t<E, 8, 1, VEC>(g, nwy, tiles, sums_only, st)
+         : cls == 1 ? rec_t<E, 16, 1, VEC>(g, nwy, tiles, sums_only, st)
+                    : rec_t<E, 16, 2, VEC>(g, nwy, tiles, sums_only, st);
 }
 template <typename E>
 cudaError_t step_e(const StepArgs &s, cudaStream_t st) {
@@ -495,12 +497,14 @@ cudaError_t step_e(const StepArgs &s, cudaStream_t st) {
 // Rows in one warp (32 or 64), or two warps of 64.
 int rec_class(int X) { return X <= 32 ? 0 : X <= 64 ? 1 : 2; }
 int64_t rec_segments(int64_t BH, int64_t T, int X, int Y, int npass, int sms) {
-  // In cycles: a position takes a warp of 64 rows about 150 of its scheduler's,
-  // and at least 300 from one to the next; 12 warps fit an SM at a time.  A
-  // head in several segments costs its sums (half of that again), the scan and
-  // a launch more.
+  // In cycles, measured: a position takes a warp of 64 rows about 290 of its
+  // scheduler's, and at least 330 from one to the next; 12 warps fit an SM at
+  // a time.  A head in several segments costs its sums (half of that again),
+  // the scan and a launch more.  (8 x 1024 x 12 heads of 64: forward 186 us in
+  // one segment, 91 in the 6 that this gives; backward 190 us in the one that it
+  // gives, 237 in 2.)
   const int64_t warps = npass * BH * ((Y + 31) / 32) * (X <= 64 ? 1 : 2);
-  const double each = X <= 32 ? 75. : 150., chain = X <= 32 ? 200. : 300.;
+  const double each = X <= 32 ? 160. : 290., chain = X <= 32 ? 220. : 330.;
   int64_t best = 1;
   double least = 1e300;
   for (int64_t n = 1; n <= std::max<int64_t>(1, std::min<int64_t>(T / 32, 12 * sms)); ++n) {
