@@ -821,7 +821,7 @@ bool encode(CUtensorMap *m, const View &v, const Pass &p, int width) {
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 bool rows16(const View &v, const Pass &p, bool tma) {
-  auto fits = [&](int64_t s, int64_t n) { return n <= 1 || (s % 8 == 0 && (!tma || s > 0)); };
+  auto fits = [&](int64_t s, int64_t n) { return n <= 1 || (s % 8 == 0 && (!tma || (s > 0 && s < (int64_t(1) << 39)))); };
   return ((uintptr_t)v.p & 15u) == 0 && fits(v.sb, p.B) && fits(v.st, p.T) && fits(v.sh, p.H);
 }
 template <int XP, int YP, bool OUT>

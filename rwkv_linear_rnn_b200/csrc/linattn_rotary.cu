@@ -6,7 +6,7 @@
 // would lose whole radians from about 2^20 on), the remainder goes to
 // sincospi in float32.  Every element is read once and written once, 16 bytes
 // at a time when the layout allows: the kernel is bound by HBM.  A block has up
-// to 1024 items of one or a few positions, so that a sine and cosine serve all
+// to 512 items of one or a few positions, so that a sine and cosine serve all
 // heads of q and k; a thread's four items are on their way before the sines are
 // computed, and everything per item is 32-bit arithmetic without a division.
 #include <algorithm>
@@ -35,12 +35,13 @@ struct Args {
   float mscale;
   int inverse;
   int pairs, items;   // of a head: items that turn, all items
+  int tail;           // elements that an item behind the pairs copies
   int tokens, parts;  // positions of a block, or blocks of a position's items
   int share;          // items of such a block
   uint32_t by_tok, by_head;  // for divisions by a position's and a head's items
 };
 
-constexpr int kThreads = 256, kItems = 4;
+constexpr int kThreads = 128, kItems = 4;
 // e / d for e d < 2^32 with m = ceil(2^32 / d); 0 stands for d = 1.
 __device__ __forceinline__ uint32_t divide(uint32_t e, uint32_t m) { return m ? __umulhi(e, m) : e; }
 
@@ -79,6 +80,14 @@ struct Pack<uint16_t, 8> {
   }
 };
 template <>
+struct Pack<uint16_t, 4> {
+  typedef uint2 Raw;
+  static __device__ __forceinline__ void get(const Raw &v, float (&x)[4]) {
+    x[0] = lo16(v.x), x[1] = hi16(v.x), x[2] = lo16(v.y), x[3] = hi16(v.y);
+  }
+  static __device__ __forceinline__ Raw put(const float (&x)[4]) { return make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3])); }
+};
+template <>
 struct Pack<float, 1> {
   typedef float Raw;
   static __device__ __forceinline__ void get(const Raw &v, float (&x)[1]) { x[0] = v; }
@@ -93,7 +102,8 @@ struct Pack<uint16_t, 1> {
 
 // One item of a head: V pairs in the half layout (elements V j.. and
 // V j + R/2..); V/2 pairs in the interleaved one (2 elements there when V = 1);
-// or, behind the pairs, V elements to copy.
+// or, behind the pairs, V elements to copy (2 V if the item's registers and the
+// head's size allow).
 template <typename E, int V, bool INTER>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Args a) {
   typedef Pack<E, V> P;
@@ -112,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   Raw x[kItems][TWO ? 2 : 1];
   E *dst[kItems];
   uint32_t wi[kItems];  // the item's first entry of cs, or a mark
-  constexpr uint32_t kCopy = ~0u, kNone = ~1u;
+  constexpr uint32_t kNone = ~0u, kCopy = ~1u, kCopy2 = ~2u;
 #pragma unroll
   for (int n = 0; n < kItems; ++n) {
     const uint32_t e = from + n * kThreads + threadIdx.x;
@@ -134,9 +144,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       if constexpr (TWO) x[n][1] = *reinterpret_cast<const Raw *>(src + (INTER ? x0 + 1 : x0 + half));
       dst[n] += x0;
     } else if (is_q ? a.copy_q : a.copy_k) {
-      const uint32_t x0 = a.R + V * (j - a.pairs);
-      wi[n] = kCopy;
+      const uint32_t x0 = a.R + a.tail * (j - a.pairs);
+      wi[n] = a.tail > V ? kCopy2 : kCopy;
       x[n][0] = *reinterpret_cast<const Raw *>(src + x0);
+      if constexpr (TWO)
+        if (a.tail > V) x[n][1] = *reinterpret_cast<const Raw *>(src + x0 + V);
       dst[n] += x0;
     }
   }
@@ -155,8 +167,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 #pragma unroll
   for (int n = 0; n < kItems; ++n) {
     if (wi[n] == kNone) continue;
-    if (wi[n] == kCopy) {
+    if (wi[n] == kCopy || wi[n] == kCopy2) {
       *reinterpret_cast<Raw *>(dst[n]) = x[n][0];
+      if constexpr (TWO)
+        if (wi[n] == kCopy2) *reinterpret_cast<Raw *>(dst[n] + V) = x[n][1];
       continue;
     }
     const float2 *w = cs + wi[n];
@@ -198,7 +212,8 @@ template <typename E, int V>
 cudaError_t launch(Args a, bool inter, cudaStream_t st) {
   const int W = inter ? (V == 1 ? 2 : V) : V;
   a.pairs = inter ? a.R / W : a.R / 2 / V;
-  a.items = a.pairs + (a.copy_q || a.copy_k ? (a.D - a.R) / V : 0);
+  a.tail = (!inter || V == 1) && (a.D - a.R) % (2 * V) == 0 ? 2 * V : V;
+  a.items = a.pairs + (a.copy_q || a.copy_k ? (a.D - a.R) / a.tail : 0);
   const int64_t per_tok = (int64_t)(a.Hq + a.Hk) * a.items, most = kThreads * kItems, half = a.R / 2;
   // few positions: fewer items each, over more blocks, to shorten the call
   int64_t want = most;
@@ -237,8 +252,8 @@ View view(const linattn_view *v) { return View{v->ptr, v->stride_b, v->stride_t,
 bool same(const linattn_view *x, const linattn_view *y) {
   return x->ptr == y->ptr && x->stride_b == y->stride_b && x->stride_t == y->stride_t && x->stride_h == y->stride_h;
 }
-// 16-byte accesses: every row of every head starts on 16 bytes.
-bool fits16(const View &v, int V) { return aligned(v.p, 16) && v.sb % V == 0 && v.st % V == 0 && v.sh % V == 0; }
+// Pieces of V elements: every row of every head starts on their bytes.
+bool fits(const View &v, int V, size_t es) { return aligned(v.p, V * es) && v.sb % V == 0 && v.st % V == 0 && v.sh % V == 0; }
 }  // namespace
 
 extern "C" int linattn_rotary(int64_t B, int64_t T, int D, int R, int dtype, int64_t Hq, const linattn_view *q,
@@ -271,12 +286,16 @@ extern "C" int linattn_rotary(int64_t B, int64_t T, int D, int R, int dtype, int
   a.copy_q = a.q.p != a.oq.p, a.copy_k = Hk && a.k.p != a.ok.p;
   a.pos = positions, a.pos64 = pos_bytes == 8, a.pos_sb = pos_stride_b;
   a.inv_freq = inv_freq, a.mscale = mscale, a.inverse = inverse;
-  const int V = dtype == WKV_F32 ? 4 : 8;
-  bool vec = D % V == 0 && R % (interleaved ? V : 2 * V) == 0;
-  for (const View *x : {&a.q, &a.oq, &a.k, &a.ok}) vec = vec && fits16(*x, V);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool inter = interleaved != 0;
-  const cudaError_t e = dtype == WKV_F32 ? (vec ? launch<float, 4>(a, inter, st) : launch<float, 1>(a, inter, st))
-                                         : (vec ? launch<uint16_t, 8>(a, inter, st) : launch<uint16_t, 1>(a, inter, st));
+  auto pieces = [&](int V) {
+    bool ok = D % V == 0 && R % (inter ? V : 2 * V) == 0;
+    for (const View *x : {&a.q, &a.oq, &a.k, &a.ok}) ok = ok && fits(*x, V, es);
+    return ok;
+  };
+  // 16 bytes, else 8 of bfloat16 (R / 2 an odd multiple of 4, as in 40 of 80), else one element
+  cudaError_t e;
+  if (dtype == WKV_F32) e = pieces(4) ? launch<float, 4>(a, inter, st) : launch<float, 1>(a, inter, st);
+  else e = pieces(8) ? launch<uint16_t, 8>(a, inter, st) : pieces(4) ? launch<uint16_t, 4>(a, inter, st) : launch<uint16_t, 1>(a, inter, st);
   return e == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
 }
