@@ -130,8 +130,9 @@ int linattn_backward_saved(int64_t BH, int64_t N, int D, int M, const void *q, c
  * - Element type `dtype` of q, k, v, out and their gradients: WKV_F32 or
  *   WKV_BF16 (float32 arithmetic, one rounding to nearest even at the end;
  *   bfloat16 products run on the tensor cores, where the masked scores and
- *   the copy of the state that q meets are rounded to bfloat16; the state
- *   itself is always float32).
+ *   the copy of the state that q meets are rounded to bfloat16.  The state
+ *   itself is always float32; there its decayed keys enter as sums of two
+ *   bfloat16 terms, 16 bits: about 4e-6 of a state that is handed out).
  * - Tensors [B, T, H, D] (q, k) and [B, T, H, M] (v, out) are given as
  *   linattn_view: a device pointer and the strides, in elements, of batch,
  *   time and head; the feature index is contiguous.  Strides are >= 0; those
@@ -139,8 +140,8 @@ int linattn_backward_saved(int64_t BH, int64_t N, int D, int M, const void *q, c
  *   and slices of a fused projection need no copy.
  * - Head sizes: 1 <= D, M <= 128.  The tensor-core kernels run when dtype is
  *   WKV_BF16, D and M are multiples of 8, pointers are 16-byte aligned,
- *   strides are multiples of 8 elements and > 0, and T is above 32; other
- *   calls run the recurrence on the CUDA cores.
+ *   strides are multiples of 8 elements, > 0 and below 2^39, and T is above
+ *   32; other calls run the recurrence on the CUDA cores.
  * - Sizes: B, H >= 1, B * H < 2^24 (N * H < 2^31 for the step), 0 <= T < 2^31.
  * - log_decay [H] float32, at most 0 (minus infinity allowed: lam = 0).  It is
  *   a constant: no call returns a gradient for it.

@@ -12,7 +12,6 @@ namespace {
 using namespace wkv;
 using namespace wkv::decay;
 
-int rc_of(cudaError_t e) { return e == cudaSuccess ? WKV_OK : WKV_ERR_CUDA; }
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 size_t elem(int dtype) { return dtype == WKV_F32 ? 4 : 2; }
 
@@ -133,7 +132,7 @@ cudaError_t run_passes(const Pass *p, int n, const Dims &d, void *ws, cudaStream
 int pass_state_through(const Dims &d, const float *in, float *out, cudaStream_t st) {
   if (!out || in == out) return WKV_OK;
   const size_t bytes = sizeof(float) * d.B * d.H * d.D * d.M;
-  return rc_of(in ? cudaMemcpyAsync(out, in, bytes, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(out, 0, bytes, st));
+  return cuda_status(in ? cudaMemcpyAsync(out, in, bytes, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(out, 0, bytes, st));
 }
 }  // namespace
 
@@ -170,7 +169,7 @@ extern "C" int linattn_decay_forward(int64_t B, int64_t T, int64_t H, int D, int
   p.a = view(q), p.b = view(k), p.c = view(v), p.o = view(out);
   p.log_decay = log_decay, p.lengths = lengths, p.s_in = state_in, p.s_out = state_out;
   p.si = scale, p.sk = 1.f, p.status = status;
-  return rc_of(run_passes(&p, 1, d, ws, st));
+  return cuda_status(run_passes(&p, 1, d, ws, st));
 }
 
 extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, int M, int dtype, const linattn_view *q,
@@ -227,7 +226,7 @@ extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, in
   p[2].a = view(k), p[2].b = view(q), p[2].c = view(grad_out), p[2].o = view(grad_v);
   p[2].s_in = grad_state_out, p[2].s_out = grad_state_in;
   p[2].si = 1.f, p[2].sk = scale, p[2].reverse = 1;
-  return rc_of(run_passes(p, 3, d, ws, st));
+  return cuda_status(run_passes(p, 3, d, ws, st));
 }
 
 extern "C" int linattn_decay_step(int64_t N, int64_t H, int D, int M, int dtype, const linattn_view *q,
@@ -250,5 +249,5 @@ extern "C" int linattn_decay_step(int64_t N, int64_t H, int D, int M, int dtype,
   if (!aligned(log_decay, 4) || !aligned(state_in, 16) || !aligned(state_out, 16)) return WKV_ERR_UNSUPPORTED;
   if (state_in != state_out && overlap(state_in, state_out, sizeof(float) * N * H * D * M)) return WKV_ERR_UNSUPPORTED;
   const decay::StepArgs s{N, H, D, M, view(&w[0]), view(&w[1]), view(&w[2]), view(&w[3]), log_decay, scale, state_in, state_out};
-  return rc_of(launch_step(s, dtype, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_step(s, dtype, static_cast<cudaStream_t>(stream)));
 }

@@ -55,6 +55,12 @@ int cuda_rc(cudaError_t e) {
   return WKV_ERR_CUDA;
 }
 
+}  // namespace
+
+int wkv::cuda_status(cudaError_t e) { return cuda_rc(e); }
+
+namespace {
+
 constexpr int64_t kDefaultSpin = 1000000;  // polls of ~1 us backoff: about one second
 constexpr int64_t kSeqMinChains = 148 * 1024;  // chains that fill B200 with one thread each
 

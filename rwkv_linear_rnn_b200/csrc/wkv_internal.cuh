@@ -51,6 +51,8 @@ inline cudaError_t launch_kernel(void (*kern)(P...), dim3 grid, dim3 block, size
 // memory limit as far as needed and asks the occupancy calculator; the answer
 // is remembered, so later launches make no runtime call for it.
 cudaError_t blocks_per_sm(const void *kern, int threads, int smem, int *blocks);
+// A call's return code; an error is kept for wkv_last_cuda_error.
+int cuda_status(cudaError_t e);
 
 // ---------------------------------------------------------------- math ---
 __device__ __forceinline__ float ex2(float x) {
