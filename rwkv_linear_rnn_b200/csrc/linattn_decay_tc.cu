@@ -35,13 +35,13 @@
 // The floor is HBM: a chunk of 128 x (X + X + Y + Y) bfloat16 takes 2.9 us of
 // an SM's share of the measured bandwidth at X = Y = 128; its MMAs take 1.4 us.
 // Measured: 3.3 us a chunk (8 x 4096 x 16 heads of 128: forward 105 to 112 us,
-// 4.8 to 5.1 TB/s; backward 303 to 318 us), 2.3 us at X = Y = 64.  A chunk is
+// 4.8 to 5.1 TB/s; backward 303 to 318 us), 2.2 us at X = Y = 64.  A chunk is
 // the chain scores, P, P c, outputs read, next a R, with the state's step beside
 // it, and the loads' latency under load is 1.9 us; the tensor pipe is busy 37 %
 // of the time and the schedulers 42 %.  What it took, at X = Y = 128: the MMA
 // warp whole under an election (an MMA in 64 cycles, not 130) and its operands
-// known uniform; every role without spills and in short loops (the GPC's
-// instruction cache was 82 % busy); masks as bits; the state never waiting for
+// known uniform; roles without spills (one word is left at X = 128) and in short
+// loops (the GPC's instruction cache was 82 % busy); masks as bits; the state never waiting for
 // the keys: 177 -> 108 us forward.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -160,12 +160,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // Shared-memory matrix descriptors of tiles in the 128-byte swizzle: rows of
 // 64 bfloat16 (128 bytes), wider tiles as consecutive halves of `rows` rows.
 // The upper word is the same for all (1024 bytes between groups of 8 rows);
@@ -483,45 +477,48 @@ __device__ __forceinline__ void scores_role(const Pass &p, Bars *s, const Chunks
     const int nv = ch.valid(it);
     if (!wait_warp(s->scores, it & 1, s, p.status)) return;
     tc_after_sync();
-    // 16 columns at a time, k = k0 .. k1 - 1 of the half's 4; P is zero in the
-    // others (written last: its columns are those of scores)
-    const int k0 = p.reverse ? min(max(2 * (w - 2 * half), 0), 4) : 0;
-    const int k1 = p.reverse ? max(min(4, (nv - 64 * half + 15) >> 4), k0) : min(max(2 * (w - 2 * half + 1), 0), 4);
-    tmem_each16(tm, k0, k1, [&](int k, uint32_t(&v)[16]) {
-          const int c0 = 64 * half + 16 * k, cb = c0 >> 5, q0 = c0 & 16;  // from column c0 on, of the block cb of 32
-          uint32_t out[8];
-          uint32_t keep = (cb == w ? causal : ~0u) >> q0;
-          if (c0 + 16 > nv) keep &= nv > c0 ? (1u << (nv - c0)) - 1u : 0u;  // what lies behind the last position may be anything
-          // lam^{|i-j|} as a factor of the row and one of the column; on the
-          // diagonal the row's is up to lam^{-31}, so strong decays take the
-          // product from a table there
-          const int i = 32 * (w - cb) + lane;
-          const f2 e = both(f * ex2(g2 * (float)(p.reverse ? -i : i - 31)));
-          if (cb == w || c0 + 16 > nv) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) v[r] = (keep >> r) & 1u ? v[r] : 0u;
-          }
-          if (cb == w && !moderate) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const int n0 = p.reverse ? q0 + 2 * r - lane : lane - 2 * r - q0, n1 = p.reverse ? n0 + 1 : n0 - 1;
-              out[r] = pack2(__uint_as_float(v[2 * r]) * (f * s->up[max(n0, 0)]),
-                             __uint_as_float(v[2 * r + 1]) * (f * s->up[max(n1, 0)]));
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const ulonglong2 z = *reinterpret_cast<const ulonglong2 *>(tab + q0 + 4 * q);
-              out[2 * q] = pack2(mul2(pair_at(v + 4 * q), mul2(e, z.x)));
-              out[2 * q + 1] = pack2(mul2(pair_at(v + 4 * q + 2), mul2(e, z.y)));
-            }
-          }
-          tmem_st8(tm + 8 * k, out);
-        });
+    // the half's two blocks of 32 columns; their P, 16 columns each, lies where the
+    // first block's scores were, which are read by then (or not needed)
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t zero[8] = {};
-      if (k < k0 || k >= k1) tmem_st8(tm + 8 * k, zero);
+    for (int k = 0; k < 2; ++k) {
+      const int cb = 2 * half + k;
+      uint32_t out[16];
+      if (p.reverse ? cb < w || 32 * cb >= nv : cb > w) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) out[r] = 0u;
+      } else {
+        uint32_t v[32];
+        tmem_ld32_nowait(tm + 32 * k, v);
+        // lam^{|i-j|} as a factor of the row and one of the column; on the
+        // diagonal the row's is up to lam^{-31}, so strong decays take the
+        // product from a table there
+        const int i = 32 * (w - cb) + lane;
+        const f2 e = both(f * ex2(g2 * (float)(p.reverse ? -i : i - 31)));
+        tmem_wait_ld();
+        pin(v);
+        if (cb == w || 32 * cb + 32 > nv) {
+          uint32_t keep = cb == w ? causal : ~0u;
+          if (32 * cb + 32 > nv) keep &= nv > 32 * cb ? (1u << (nv - 32 * cb)) - 1u : 0u;  // what lies behind the last position may be anything
+#pragma unroll
+          for (int r = 0; r < 32; ++r) v[r] = (keep >> r) & 1u ? v[r] : 0u;
+        }
+        if (cb == w && !moderate) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int n0 = p.reverse ? 2 * r - lane : lane - 2 * r, n1 = p.reverse ? n0 + 1 : n0 - 1;
+            out[r] = pack2(__uint_as_float(v[2 * r]) * (f * s->up[max(n0, 0)]),
+                           __uint_as_float(v[2 * r + 1]) * (f * s->up[max(n1, 0)]));
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const ulonglong2 z = *reinterpret_cast<const ulonglong2 *>(tab + 4 * q);
+            out[2 * q] = pack2(mul2(pair_at(v + 4 * q), mul2(e, z.x)));
+            out[2 * q + 1] = pack2(mul2(pair_at(v + 4 * q + 2), mul2(e, z.y)));
+          }
+        }
+      }
+      tmem_st16(tm + 16 * k, out);
     }
     tmem_wait_st();
     tc_before_sync();
