@@ -124,9 +124,9 @@ cudaError_t launch_scan(const Group &g, cudaStream_t st);
 // sizes share a launch, the segments per head and their length, the launches.
 bool tc_fits(const Pass &p);
 inline bool tc_one_class(int D, int M) { return (D <= 64) == (M <= 64); }
-int64_t tc_segments(int64_t BH, int64_t T, int npass, int sms);
+int64_t tc_segments(int64_t BH, int64_t T, int X, int Y, int npass, int sms);
 int64_t tc_segment_len(int64_t T, int64_t nseg);
-cudaError_t launch_tc(const Group &g, bool sums_only, cudaStream_t st);
+cudaError_t launch_tc(const Group &g, bool sums_only, int sms, cudaStream_t st);
 struct StepArgs {
   int64_t N, H;
   int D, M;

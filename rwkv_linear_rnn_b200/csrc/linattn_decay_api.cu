@@ -78,7 +78,7 @@ bool uses_tc(const Dims &d) { return d.dtype == WKV_BF16 && d.T > 32 && d.D % 8 
 size_t group_bytes(const Dims &d, int X, int Y, int n) {
   const int64_t BH = d.B * d.H;
   const size_t rec = seg_bytes(d, rec_segments(BH, d.T, X, Y, n, num_sms()));
-  return n * (uses_tc(d) ? std::max(rec, seg_bytes(d, tc_segments(BH, d.T, n, num_sms()))) : rec);
+  return n * (uses_tc(d) ? std::max(rec, seg_bytes(d, tc_segments(BH, d.T, X, Y, n, num_sms()))) : rec);
 }
 // Groups run one after the other and share the workspace.  A backward's
 // passes are one group or, with heads of two classes, {grad_q, grad_k} and
@@ -99,14 +99,14 @@ cudaError_t run_group(Group &g, const Dims &d, bool tc, void *ws, cudaStream_t s
   int X = 0, Y = 0;
   for (int i = 0; i < g.n; ++i) X = std::max(X, g.p[i].X), Y = std::max(Y, g.p[i].Y);
   const int64_t BH = d.B * d.H;
-  const int64_t nseg = tc ? tc_segments(BH, d.T, g.n, num_sms()) : rec_segments(BH, d.T, X, Y, g.n, num_sms());
+  const int64_t nseg = tc ? tc_segments(BH, d.T, X, Y, g.n, num_sms()) : rec_segments(BH, d.T, X, Y, g.n, num_sms());
   for (int i = 0; i < g.n; ++i) {
     Pass &p = g.p[i];
     p.nseg = (int)nseg;
     p.seg_len = tc ? tc_segment_len(d.T, nseg) : (d.T + nseg - 1) / nseg;
     p.seg = static_cast<float *>(ws) + i * (seg_bytes(d, nseg) / sizeof(float));
   }
-  auto launch = [&](bool sums_only) { return tc ? launch_tc(g, sums_only, st) : launch_rec(g, d.dtype, sums_only, st); };
+  auto launch = [&](bool sums_only) { return tc ? launch_tc(g, sums_only, num_sms(), st) : launch_rec(g, d.dtype, sums_only, st); };
   cudaError_t e = cudaSuccess;
   if (nseg > 1) {
     e = launch(true);

@@ -26,7 +26,8 @@
 //
 // One CTA runs one head's segment with specialised warps: a producer (TMA
 // loads), an MMA issuer, a warpgroup for the state (its bfloat16 copy and its
-// decay), one for the outputs, two for P, one for the weighted keys.  The MMAs
+// decay), one for the outputs, two for P, one for the weighted keys (fewer where
+// two CTAs share an SM).  The MMAs
 // of a chunk are issued in the order scores, keys (first term), a R, keys
 // (second term), P c, so that each step of a warpgroup has the products of
 // others to hide behind: P behind keys and a R, the state's step behind P c and
@@ -57,7 +58,6 @@ namespace decay {
 
 constexpr int kL = 128;                  // positions per chunk
 constexpr uint32_t kHalf = kL * 128;     // bytes of 128 rows of 64 bfloat16
-constexpr uint32_t kTmemCols = 512;
 constexpr int kMostSlots = 8;             // of the ring of tiles
 constexpr uint32_t kTries = 1u << 23;    // bound on any one wait
 
@@ -223,17 +223,29 @@ __device__ __forceinline__ float power(float g2, int n) { return n == 0 ? 1.f : 
 // slot: with five slots c waits for the a of the chunk before it, a and b for b
 // and c of the one before that.  With X = 64 the state's products run with
 // M = 128: their rows from 64 on are the bytes behind the keys (there always
-// are some) and their results are not read.
-template <int XP, int YP, bool OUT>
+// are some; TWO: the keys again) and their results are not read.
+//
+// TWO (X = Y = 64): two CTAs on an SM, each with half of its shared memory,
+// tensor memory and registers, so that one's chain of steps fills the other's
+// waits; the rule for it is at the launch.
+template <int XP, int YP, bool OUT, bool TWO>
 struct Tiles {
   static constexpr uint32_t BT = XP / 64 * kHalf, CT = YP / 64 * kHalf, RT = OUT ? YP / 64 * XP * 128 : 0;
   static constexpr uint32_t SLOT = BT > CT ? BT : CT;
-  static constexpr uint32_t MOST = 224 * 1024;
+  static constexpr uint32_t MOST = TWO ? 104 * 1024 : 224 * 1024;
   static constexpr int FIT = (int)((MOST - BT - RT) / SLOT), NS = FIT < kMostSlots ? FIT : kMostSlots;
   static constexpr int PER = OUT ? 3 : 2;  // tiles of a chunk: (a,) b, c
   static constexpr uint32_t R = 0, W = RT, RING = W + BT, BYTES = RING + NS * SLOT;
   static_assert(NS >= 5 && BYTES <= MOST, "the ring holds a chunk and more; the rows behind a b of the last slot exist");
-  static_assert(XP == 128 || SLOT > BT || BYTES + BT <= MOST, "");
+  static_assert(XP == 128 || TWO || SLOT > BT || BYTES + BT <= MOST, "");
+};
+
+// Columns of tensor memory.  TWO: O1 (P c) lies between P's halves, where
+// scores were, so that two CTAs' share is enough.
+template <int YP, bool TWO>
+struct Cols {
+  static constexpr uint32_t SCORES = 0, O1 = TWO ? 32 : 128, O2 = TWO ? 128 : 128 + YP, ST = O2 + YP, ALL = TWO ? 256 : 512;
+  static_assert(ST + YP <= ALL && (!TWO || YP == 64), "");
 };
 
 struct Bars {
@@ -252,14 +264,16 @@ struct Bars {
   alignas(16) float up[32];  // lam^r, lam^{31-r}; read four at a time
   alignas(16) float down[32];
 };
-constexpr int kKeyThreads = 128, kScoreWarps = 8;
-// Warps of a CTA: 4 state, (4 outputs, 8 P,) 4 keys, loads, MMAs.  Their hot
+constexpr int kKeyThreads = 128;
+// Warps of a CTA: 4 state, (4 outputs, 8 P,) 4 keys, loads, MMAs; TWO: 2 state,
+// loads, MMAs, 4 P and outputs, 4 keys.  Their hot
 // loops are kept short: one that does not fit the instruction cache with the
 // others waits for its instructions, chunk after chunk.  Nor may a register
 // spill: shared memory takes L1's place and a reload is a trip to L2.
-template <bool OUT>
+template <bool OUT, bool TWO>
 struct Roles {
-  static constexpr int KEYS = OUT ? 16 : 4, LOAD = KEYS + 4, MMA = LOAD + 1, THREADS = 32 * (MMA + 1);
+  static constexpr int STATE = TWO ? 2 : 4, SCORES = TWO ? 4 : 8, KEYS = TWO ? 8 : OUT ? 16 : 4;
+  static constexpr int LOAD = TWO ? 2 : KEYS + 4, MMA = LOAD + 1, THREADS = TWO ? 384 : 32 * (MMA + 1);
 };
 
 // Waits for the phase of `addr` with the given parity, in at most kTries tries
@@ -313,13 +327,13 @@ struct Chunks {
 
 // State warpgroup: R at the chunk's start -> its bfloat16 copy in shared memory
 // and, decayed, tensor memory again.  A thread is a row of the state.
-template <int XP, int YP, bool OUT>
+template <int XP, int YP, bool OUT, bool TWO>
 __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int64_t unit, float g,
                                            float *result) {
-  using Ti = Tiles<XP, YP, OUT>;
+  using Ti = Tiles<XP, YP, OUT, TWO>;
   const int x = threadIdx.x, warp = x >> 5;
   const int64_t bh = unit / p.nseg;
-  const uint32_t tm = s->tmem + 128 + 2 * YP + ((uint32_t)(32 * warp) << 16);
+  const uint32_t tm = s->tmem + Cols<YP, TWO>::ST + ((uint32_t)(32 * warp) << 16);
   const bool rows = 32 * warp < XP;  // this warp's lanes hold state rows
   const int64_t XY = (int64_t)p.X * p.Y;
   const float *init = !OUT ? nullptr : p.nseg > 1 ? p.seg + unit * XY : p.s_in ? p.s_in + bh * XY : nullptr;
@@ -405,10 +419,10 @@ __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, 
 
 // Key warpgroup: lam^n b as two bfloat16 terms, the second in b's place once
 // its scores are formed; a thread has a row (position).
-template <int XP, int YP, bool OUT>
+template <int XP, int YP, bool OUT, bool TWO>
 __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, float g2, bool more) {
-  using Ti = Tiles<XP, YP, OUT>;
-  const int j = threadIdx.x - 32 * Roles<OUT>::KEYS;
+  using Ti = Tiles<XP, YP, OUT, TWO>;
+  const int j = threadIdx.x - 32 * Roles<OUT, TWO>::KEYS;
   Place<Ti::NS> place;
   // One term: f of every pair of the tile at src.
   auto convert = [&](const uint8_t *src, uint8_t *dst, uint64_t &full, auto f) {
@@ -463,32 +477,38 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
 }
 
 // P warpgroups: the masked, weighted scores, rounded to bfloat16, in tensor
-// memory over the scores' own columns; a thread has a row and half its columns,
-// and the halves' P lies at columns 0 and 64.
-__device__ __forceinline__ void scores_role(const Pass &p, Bars *s, const Chunks &ch, float g2) {
-  const int t = threadIdx.x & 255, w = (t >> 5) & 3, lane = t & 31, half = t >> 7;
-  const uint32_t tm = s->tmem + ((uint32_t)(32 * w) << 16) + 64 * half;
-  const float f = p.si * p.sk;
-  const bool moderate = g2 * 31.f > -100.f;
-  const uint32_t causal = p.reverse ? ~0u << lane : (2u << lane) - 1u;  // columns of the diagonal block that count
-  const float *tab = p.reverse ? s->up : s->down;
-#pragma unroll 1
-  for (int it = 0; it < ch.n; ++it) {
+// memory over the scores' own columns; a thread has a row and half its columns
+// (TWO: all of them), and the halves' P lies at columns 0 and 64 (TWO: 96).
+template <bool TWO>
+struct Scores {
+  const Pass &p;
+  float g2, f;
+  int w, lane, half;
+  uint32_t tm;
+  __device__ __forceinline__ Scores(const Pass &p, const Bars *s, float g2) : p(p), g2(g2), f(p.si * p.sk) {
+    const int t = threadIdx.x & 255;
+    w = (t >> 5) & 3, lane = t & 31, half = TWO ? 0 : t >> 7;
+    tm = s->tmem + ((uint32_t)(32 * w) << 16);
+  }
+  __device__ __forceinline__ bool chunk(Bars *s, const Chunks &ch, int it) const {
+    const bool moderate = g2 * 31.f > -100.f;
+    const uint32_t causal = p.reverse ? ~0u << lane : (2u << lane) - 1u;  // columns of the diagonal block that count
+    const float *tab = p.reverse ? s->up : s->down;
     const int nv = ch.valid(it);
-    if (!wait_warp(s->scores, it & 1, s, p.status)) return;
+    if (!wait_warp(s->scores, it & 1, s, p.status)) return false;
     tc_after_sync();
-    // the half's two blocks of 32 columns; their P, 16 columns each, lies where the
-    // first block's scores were, which are read by then (or not needed)
+    // blocks of 32 columns; the P of two, 16 columns each, lies where the first's
+    // scores were, which are read by then (or not needed)
 #pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-      const int cb = 2 * half + k;
+    for (int k = 0; k < (TWO ? 4 : 2); ++k) {
+      const int cb = TWO ? k ^ (k >> 1) : 2 * half + k;  // TWO: 0, 1, 3, 2
       uint32_t out[16];
       if (p.reverse ? cb < w || 32 * cb >= nv : cb > w) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) out[r] = 0u;
       } else {
         uint32_t v[32];
-        tmem_ld32_nowait(tm + 32 * k, v);
+        tmem_ld32_nowait(tm + 32 * cb, v);
         // lam^{|i-j|} as a factor of the row and one of the column; on the
         // diagonal the row's is up to lam^{-31}, so strong decays take the
         // product from a table there
@@ -518,31 +538,38 @@ __device__ __forceinline__ void scores_role(const Pass &p, Bars *s, const Chunks
           }
         }
       }
-      tmem_st16(tm + 16 * k, out);
+      tmem_st16(tm + (TWO ? 16 * cb + (cb >> 1) * 64 : 64 * half + 16 * k), out);
     }
     tmem_wait_st();
     tc_before_sync();
     arrive_warp(s->p_ready);
+    return true;
   }
-}
+};
 
 // Output warpgroup, a thread per row: P c + weight x (a R), rounded and stored
 // as 16- or 32-byte pieces of the row.
-template <int YP>
-__device__ __forceinline__ void output_role(const Pass &p, Bars *s, const Chunks &ch, int64_t b, int64_t h, float g2,
-                                            bool wide) {
-  const int i = threadIdx.x & 127;
-  const uint32_t tm = s->tmem + 128 + ((uint32_t)(i & ~31) << 16);
-  for (int it = 0; it < ch.n; ++it) {
-    const int nv = ch.valid(it);
+template <int YP, bool TWO>
+struct Outputs {
+  const Pass &p;
+  float g2;
+  bool wide;
+  uint32_t tm;
+  uint16_t *row;  // of position 0
+  __device__ __forceinline__ Outputs(const Pass &p, const Bars *s, int64_t b, int64_t h, float g2, bool wide)
+      : p(p), g2(g2), wide(wide), tm(s->tmem + ((threadIdx.x & 96u) << 16)),
+        row(static_cast<uint16_t *>(const_cast<void *>(p.o.p)) + b * p.o.sb + h * p.o.sh) {}
+  __device__ __forceinline__ bool chunk(Bars *s, const Chunks &ch, int it) const {
+    constexpr uint32_t O1 = Cols<YP, TWO>::O1, O2 = Cols<YP, TWO>::O2;
+    const int i = threadIdx.x & 127, nv = ch.valid(it);
     const f2 w = both(i < nv ? p.si * power(g2, p.reverse ? nv - 1 - i : i + 1) : 0.f);
     const int64_t t = (int64_t)ch.start(it) + i;
-    uint16_t *dst = static_cast<uint16_t *>(const_cast<void *>(p.o.p)) + b * p.o.sb + h * p.o.sh + t * p.o.st;
-    if (!wait_warp(s->o_done, it & 1, s, p.status)) return;
+    uint16_t *dst = row + t * p.o.st;
+    if (!wait_warp(s->o_done, it & 1, s, p.status)) return false;
     tc_after_sync();
     uint32_t o1[16], o2[16], z[8];
-    tmem_ld16_nowait(tm, o1);
-    tmem_ld16_nowait(tm + YP, o2);
+    tmem_ld16_nowait(tm + O1, o1);
+    tmem_ld16_nowait(tm + O2, o2);
 #pragma unroll 1
     for (int y = 0; y < YP; y += 16) {
       tmem_wait_ld();
@@ -557,8 +584,8 @@ __device__ __forceinline__ void output_role(const Pass &p, Bars *s, const Chunks
         for (int r = 0; r < 8; ++r) z[r] = i < nv ? z[r] : 0u;
       }
       if (y < YP - 16) {
-        tmem_ld16_nowait(tm + y + 16, o1);
-        tmem_ld16_nowait(tm + YP + y + 16, o2);
+        tmem_ld16_nowait(tm + O1 + y + 16, o1);
+        tmem_ld16_nowait(tm + O2 + y + 16, o2);
       } else {
         tc_before_sync();
         arrive_warp(s->o_free);
@@ -574,15 +601,16 @@ __device__ __forceinline__ void output_role(const Pass &p, Bars *s, const Chunks
       }
       __syncwarp();
     }
+    return true;
   }
-}
+};
 
 // Loads: the tiles of each chunk in the ring's order, each as soon as its slot
 // is free; one whole warp.
-template <int XP, int YP, bool OUT>
+template <int XP, int YP, bool OUT, bool TWO>
 __device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, int b, int h,
                                           const CUtensorMap *am, const CUtensorMap *bm, const CUtensorMap *cm) {
-  using Ti = Tiles<XP, YP, OUT>;
+  using Ti = Tiles<XP, YP, OUT, TWO>;
   Place<Ti::NS> place;
   int n = 0;  // tiles whose loads were issued
   bool ok = true;
@@ -611,10 +639,11 @@ __device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, c
 }
 
 // MMAs, in the order that the head of this file explains; one whole warp.
-template <int XP, int YP, bool OUT>
+template <int XP, int YP, bool OUT, bool TWO>
 __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, bool more) {
-  using Ti = Tiles<XP, YP, OUT>;
-  constexpr uint32_t SCORES = 0, O1 = 128, O2 = 128 + YP, ST = 128 + 2 * YP;
+  using Ti = Tiles<XP, YP, OUT, TWO>;
+  using Co = Cols<YP, TWO>;
+  constexpr uint32_t SCORES = Co::SCORES, O1 = Co::O1, O2 = Co::O2, ST = Co::ST;
   const uint32_t tm = __shfl_sync(~0u, s->tmem, 0);
   auto loaded = [&](const Place<Ti::NS> &t) { return wait_warp(s->full[t.slot], t.phase, s, p.status); };
   auto tile = [&](const Place<Ti::NS> &t) { return sm + Ti::RING + t.slot * Ti::SLOT; };
@@ -629,6 +658,10 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
     const int n_terms = more || it + 1 < ch.n ? 2 : 0;
     if (OUT) {
       if (!(ok = loaded(na) && loaded(nb))) break;
+      if (TWO && it > 0) {  // the scores' columns hold O1
+        if (!(ok = wait_warp(s->o_free, ph ^ 1u, s, p.status))) break;
+        tc_after_sync();
+      }
       if (elect_one()) {
         const uint32_t da = kmajor(ta), db = kmajor(tb);
 #pragma unroll
@@ -647,7 +680,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
         if (!(ok = wait_warp(s->w_full[k], ph, s, p.status))) break;
         tc_after_sync();
         if (elect_one()) {
-          const uint32_t dw = mnmajor(k == 0 ? sm + Ti::W : tb, kHalf), dc = mnmajor(tc, kHalf);
+          const uint32_t dw = mnmajor(k == 0 ? sm + Ti::W : tb, TWO ? 0u : kHalf), dc = mnmajor(tc, kHalf);
           const bool acc = OUT || it > 0 || k > 0;
           const uint32_t id = idesc(128, YP, true, true) | (k > 0 ? kNegateA : 0u);
 #pragma unroll
@@ -658,7 +691,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
         __syncwarp();
       }
       if (OUT && k == 0) {
-        if (it > 0 && !(ok = wait_warp(s->o_free, ph ^ 1u, s, p.status))) break;
+        if (!TWO && it > 0 && !(ok = wait_warp(s->o_free, ph ^ 1u, s, p.status))) break;
         tc_after_sync();
         if (elect_one()) {
           const uint32_t da = kmajor(ta), dr = mnmajor(sm + Ti::R, XP * 128);
@@ -686,7 +719,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
         const uint32_t dc = mnmajor(tc, kHalf);
 #pragma unroll
         for (int k = 0; k < kL / 16; ++k)
-          mma_ts(tm + O1, tm + SCORES + 8 * k + (k >= 4 ? 32 : 0), dc + mnstep(k), idesc(128, YP, false, true), k > 0);
+          mma_ts(tm + O1, tm + SCORES + 8 * k + (k >= 4 ? (TWO ? 64 : 32) : 0), dc + mnstep(k), idesc(128, YP, false, true), k > 0);
         mma_commit(smem_addr(&s->o_done));
       }
       mma_commit(smem_addr(&s->empty[nc.slot]));
@@ -721,10 +754,10 @@ __device__ __forceinline__ void zero_padding(const Group &group) {
 
 // A block is a segment of a head of one pass; the passes of a segment are
 // neighbours, so that those that read the same tensors find them in L2.
-template <int XP, int YP, bool OUT>
-__global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const __grid_constant__ Maps maps,
-                                                                          const __grid_constant__ Group group) {
-  using Ro = Roles<OUT>;
+template <int XP, int YP, bool OUT, bool TWO>
+__global__ void __launch_bounds__(Roles<OUT, TWO>::THREADS, TWO ? 2 : 1) decay_tc_kernel(const __grid_constant__ Maps maps,
+                                                                                         const __grid_constant__ Group group) {
+  using Ro = Roles<OUT, TWO>;
   const int pass = (int)(blockIdx.x % (unsigned)group.n);
   const int64_t unit = blockIdx.x / (unsigned)group.n;
   const Pass &p = group.p[pass];
@@ -754,8 +787,9 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
     for (uint64_t *f : {&bars.scores, &bars.w_free, &bars.state, &bars.o_done, &bars.drain})
       mbar_init(smem_addr(f), 1);
     for (uint64_t *f : {&bars.w_full[0], &bars.w_full[1], &bars.c_clean}) mbar_init(smem_addr(f), kKeyThreads / 32);
-    mbar_init(smem_addr(&bars.p_ready), kScoreWarps);
-    for (uint64_t *f : {&bars.o_free, &bars.r_ready}) mbar_init(smem_addr(f), 4);
+    mbar_init(smem_addr(&bars.p_ready), Ro::SCORES);
+    mbar_init(smem_addr(&bars.o_free), 4);
+    mbar_init(smem_addr(&bars.r_ready), Ro::STATE);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (threadIdx.x >= 32 && threadIdx.x < 64) {
@@ -763,21 +797,36 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
     bars.up[r] = power(g2, r);
     bars.down[r] = power(g2, 31 - r);
   }
-  if (warp == 0) tmem_alloc(smem_addr(&bars.tmem), kTmemCols);
+  if (warp == 0) tmem_alloc(smem_addr(&bars.tmem), Cols<YP, TWO>::ALL);
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
-  if (warp < 4) {
-    state_role<XP, YP, OUT>(p, &bars, sm, ch, unit, g, result);
-  } else if (OUT && warp < 8) {
-    output_role<YP>(p, &bars, ch, b, h, g2, wide != 0);
-  } else if (OUT && warp < Ro::KEYS) {
-    scores_role(p, &bars, ch, g2);
-  } else if (warp < Ro::LOAD) {
-    keys_role<XP, YP, OUT>(p, &bars, sm, ch, g2, result != nullptr);
-  } else {
-    if (warp == Ro::LOAD) load_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, (int)b, (int)h, &am, &bm, &cm);
-    else mma_role<XP, YP, OUT>(p, &bars, smem_addr(sm), ch, result != nullptr);
+  if (warp < Ro::STATE) {
+    state_role<XP, YP, OUT, TWO>(p, &bars, sm, ch, unit, g, result);
+  } else if (warp == Ro::LOAD) {
+    load_role<XP, YP, OUT, TWO>(p, &bars, smem_addr(sm), ch, (int)b, (int)h, &am, &bm, &cm);
+  } else if (warp == Ro::MMA) {
+    mma_role<XP, YP, OUT, TWO>(p, &bars, smem_addr(sm), ch, result != nullptr);
+  } else if (warp >= Ro::KEYS) {
+    keys_role<XP, YP, OUT, TWO>(p, &bars, sm, ch, g2, result != nullptr);
+  } else if constexpr (TWO) {
+    const Scores<TWO> scores(p, &bars, g2);
+    const Outputs<YP, TWO> outputs(p, &bars, b, h, g2, wide != 0);
+#pragma unroll 1
+    for (int it = 0; it < ch.n; ++it)
+      if (!scores.chunk(&bars, ch, it) || !outputs.chunk(&bars, ch, it)) break;
+  } else if constexpr (OUT) {
+    if (warp < 8) {
+      const Outputs<YP, TWO> outputs(p, &bars, b, h, g2, wide != 0);
+#pragma unroll 1
+      for (int it = 0; it < ch.n; ++it)
+        if (!outputs.chunk(&bars, ch, it)) break;
+    } else {
+      const Scores<TWO> scores(p, &bars, g2);
+#pragma unroll 1
+      for (int it = 0; it < ch.n; ++it)
+        if (!scores.chunk(&bars, ch, it)) break;
+    }
   }
   __syncwarp();
   if (OUT) zero_padding(group);
@@ -785,7 +834,7 @@ __global__ void __launch_bounds__(Roles<OUT>::THREADS, 1) decay_tc_kernel(const 
   __syncthreads();
   if (warp == 0) {
     tc_after_sync();
-    tmem_dealloc(bars.tmem, kTmemCols);
+    tmem_dealloc(bars.tmem, Cols<YP, TWO>::ALL);
   }
 }
 
@@ -829,14 +878,14 @@ bool rows16(const View &v, const Pass &p, bool tma) {
   auto fits = [&](int64_t s, int64_t n) { return n <= 1 || (s % 8 == 0 && (!tma || (s > 0 && s < (int64_t(1) << 39)))); };
   return ((uintptr_t)v.p & 15u) == 0 && fits(v.sb, p.B) && fits(v.st, p.T) && fits(v.sh, p.H);
 }
-template <int XP, int YP, bool OUT>
+template <int XP, int YP, bool OUT, bool TWO = false>
 cudaError_t launch_t(const Group &g, cudaStream_t st) {
   Maps m{};
   if (!encoder() || !ensure_context()) return cudaErrorNotSupported;
-  const auto kern = decay_tc_kernel<XP, YP, OUT>;
-  constexpr int smem = (int)Tiles<XP, YP, OUT>::MOST + 1024;
+  const auto kern = decay_tc_kernel<XP, YP, OUT, TWO>;
+  constexpr int smem = (int)Tiles<XP, YP, OUT, TWO>::MOST + 1024;
   int blocks = 0;
-  const cudaError_t e = blocks_per_sm((const void *)kern, Roles<OUT>::THREADS, smem, &blocks);
+  const cudaError_t e = blocks_per_sm((const void *)kern, Roles<OUT, TWO>::THREADS, smem, &blocks);
   if (e != cudaSuccess) return e;
   if (blocks < 1) return cudaErrorInvalidConfiguration;
   auto even = [](int64_t s, int64_t n) { return n <= 1 || s % 16 == 0; };
@@ -848,11 +897,21 @@ cudaError_t launch_t(const Group &g, cudaStream_t st) {
                 even(p.o.sh, p.H);
   }
   const Pass &p = g.p[0];
-  return launch_kernel(kern, dim3((unsigned)(p.B * p.H * p.nseg * g.n)), dim3(Roles<OUT>::THREADS), smem, st, m, g);
+  return launch_kernel(kern, dim3((unsigned)(p.B * p.H * p.nseg * g.n)), dim3(Roles<OUT, TWO>::THREADS), smem, st, m, g);
 }
+// Time of the output launch when an SM has `units` CTAs of heads up to 64 to run,
+// in chunks of a CTA alone on its SM (2.2 us each): one after the other with 22
+// warps, or, with 12, two at a time (4.0 us for a chunk of each; 3.15 for the odd
+// one's).  Forward, 4096 positions: 2 units 140 us and 128, 3 units 201 and 229;
+// 2048 positions, 4 units: 151 and 130; 1024 positions, 6 units: 123 and 99.
+double unit_time(int64_t units, bool two) { return two ? 1.82 * (double)(units / 2) + 1.43 * (double)(units % 2) : (double)units; }
+bool pairs(int64_t units) { return unit_time(units, true) < unit_time(units, false); }
 template <bool OUT>
-cudaError_t launch_o(const Group &g, cudaStream_t st) {
+cudaError_t launch_o(const Group &g, int sms, cudaStream_t st) {
+  const int64_t units = (g.p[0].B * g.p[0].H * g.p[0].nseg * g.n + sms - 1) / sms;
   const int X = g.p[0].X, Y = g.p[0].Y;
+  if constexpr (OUT)
+    if (X <= 64 && Y <= 64 && pairs(units)) return launch_t<64, 64, OUT, true>(g, st);
   if (X <= 64) return Y <= 64 ? launch_t<64, 64, OUT>(g, st) : launch_t<64, 128, OUT>(g, st);
   return Y <= 64 ? launch_t<128, 64, OUT>(g, st) : launch_t<128, 128, OUT>(g, st);
 }
@@ -862,7 +921,7 @@ bool tc_fits(const Pass &p) {
   return p.X % 8 == 0 && p.Y % 8 == 0 && p.X <= 128 && p.Y <= 128 && rows16(p.a, p, true) && rows16(p.b, p, true) &&
          rows16(p.c, p, true) && rows16(p.o, p, false);
 }
-int64_t tc_segments(int64_t BH, int64_t T, int npass, int sms) {
+int64_t tc_segments(int64_t BH, int64_t T, int X, int Y, int npass, int sms) {
   BH *= npass;
   // in units of one chunk's outputs: a segment costs its chunks and about 2 for
   // starting and ending its CTA; a head in several segments also its sums (b
@@ -873,8 +932,9 @@ int64_t tc_segments(int64_t BH, int64_t T, int npass, int sms) {
   for (int64_t n = 1; n <= std::min<int64_t>(nch, std::max<int64_t>(1, 2 * sms / BH)); ++n) {
     const int64_t per = (nch + n - 1) / n;
     if ((nch + per - 1) / per != n) continue;
-    const double waves = (double)((BH * n + sms - 1) / sms);
-    const double t = waves * (per + 2.0) + (n > 1 ? waves * (0.6 * per + 2.0) + 2.0 : 0.0);
+    const int64_t units = (BH * n + sms - 1) / sms;
+    const double waves = (double)units, out = unit_time(units, X <= 64 && Y <= 64 && pairs(units));
+    const double t = out * (per + 2.0) + (n > 1 ? waves * (0.6 * per + 2.0) + 2.0 : 0.0);
     if (t < least) least = t, best = n;
   }
   return best;
@@ -883,8 +943,8 @@ int64_t tc_segment_len(int64_t T, int64_t nseg) {
   const int64_t nch = (T + kL - 1) / kL;
   return (nch + nseg - 1) / nseg * kL;
 }
-cudaError_t launch_tc(const Group &g, bool sums_only, cudaStream_t st) {
-  return sums_only ? launch_o<false>(g, st) : launch_o<true>(g, st);
+cudaError_t launch_tc(const Group &g, bool sums_only, int sms, cudaStream_t st) {
+  return sums_only ? launch_o<false>(g, sms, st) : launch_o<true>(g, sms, st);
 }
 
 }  // namespace decay

@@ -119,6 +119,27 @@ def test_segments_with_heads_of_two_sizes(D, M, dtype):
     check_backward(c)
 
 
+@pytest.mark.parametrize("D,M", [(64, 64), (40, 24), (8, 64)])
+def test_two_heads_on_a_multiprocessor(D, M):
+    """More heads of up to 64 than multiprocessors (forward 180 of them, backward 540), with every kind of
+    decay and padded rows."""
+    H = 36
+    decay = -np.exp2(-9.0 * np.arange(H) / H)
+    decay[:8] = 0.0, -1e-7, -0.5, -2.0, -5.0, -30.0, -200.0, float("-inf")
+    lengths = [300, 0, 129, 256, 1]
+    c = Case(33, len(lengths), 300, H, D, M, "bf16", state=True, decay=decay, lengths=lengths, layout="fused")
+    out = check_forward(c)
+    check_backward(c)
+    for b, n in enumerate(lengths):
+        assert not host(out)[b, n:].any()
+
+
+def test_two_heads_on_a_multiprocessor_over_many_chunks():
+    c = Case(34, 8, 1500, 20, 16, 16, "bf16", state=True)
+    check_forward(c)
+    check_backward(c)
+
+
 @pytest.mark.parametrize("T", [3, 90])
 def test_gradients_against_differences(T):
     c = Case(32, 2, T, 2, 40, 24, "f32", state=True)
