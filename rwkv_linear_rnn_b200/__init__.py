@@ -330,7 +330,7 @@ def _status_ptr(ref, dev):
             return 0
         t = ref.new_zeros(1, dtype=torch.int32)
         torch.cuda.current_stream(dev).synchronize()  # zeroed before any other stream's call stores to it
-        known = _decay_status[dev] = (t, t.data_ptr())
+        known = _decay_status.setdefault(dev, (t, t.data_ptr()))  # the first of several threads' stays
     return known[1]
 
 
@@ -338,12 +338,13 @@ def linattn_decay_status(device=None):
     """Device-side status of the ``linattn_decay_*`` calls made so far (0, or
     WKV_ERR_TIMEOUT if a bounded wait gave up); waits for the device and clears it."""
     torch = _torch()
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    known = _decay_status.get(device.index)
+    device = torch.device("cuda" if device is None else device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    known = _decay_status.get(index)
     if known is None:
         return 0
     t = known[0]
-    torch.cuda.synchronize(device)
+    torch.cuda.synchronize(index)
     rc = int(t.item())
     if rc:
         t.zero_()

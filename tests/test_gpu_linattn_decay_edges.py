@@ -14,6 +14,7 @@ import torch
 
 import rwkv_linear_rnn_b200 as W
 from oracle import linattn_decay as ld
+from rwkv_linear_rnn_b200.constants import WKV_ERR_TIMEOUT
 from test_gpu_linattn_decay import REL, STATE_REL, TYPES, Case, check_backward, check_forward, host, rel
 
 pytestmark = pytest.mark.gpu
@@ -201,3 +202,15 @@ def test_rotary_block_shapes(B, T, Hq, Hk, D, R, interleaved):
         # half a step of the result, and the pair's float32 roundings (elements are below 8)
         assert np.all(np.abs(host(y) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -21 * 12)
         assert torch.equal(y[..., R:], x[..., R:])
+
+
+def test_the_status_word_of_every_way_to_name_the_device():
+    q = torch.randn(1, 40, 2, 64, device="cuda").bfloat16()
+    W.linattn_decay_forward(q, q, q, torch.zeros(2, device="cuda"))
+    here = torch.cuda.current_device()
+    word = W._decay_status[here][0]
+    for name in (None, "cuda", f"cuda:{here}", torch.device("cuda"), q.device):
+        assert W.linattn_decay_status(name) == 0
+        word.fill_(WKV_ERR_TIMEOUT)
+        assert W.linattn_decay_status(name) == WKV_ERR_TIMEOUT, name
+        assert W.linattn_decay_status(name) == 0
