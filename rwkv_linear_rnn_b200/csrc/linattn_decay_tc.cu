@@ -39,7 +39,7 @@
 // 4.8 to 5.1 TB/s; backward 303 to 318 us), 2.2 us at X = Y = 64.  A chunk is
 // the chain scores, P, P c, outputs read, next a R, with the state's step beside
 // it, and the loads' latency under load is 1.9 us; the tensor pipe is busy 37 %
-// of the time and the schedulers 42 %.  What it took, at X = Y = 128: the MMA
+// of the time and the schedulers 40 %.  What it took, at X = Y = 128: the MMA
 // warp whole under an election (an MMA in 64 cycles, not 130) and its operands
 // known uniform; roles without spills (one word is left at X = 128) and in short
 // loops (the GPC's instruction cache was 82 % busy); masks as bits; the state never waiting for
