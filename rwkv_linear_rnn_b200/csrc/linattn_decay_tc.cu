@@ -635,7 +635,8 @@ __device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, c
   }
   // The loads in flight write shared memory that outlives this warp, not the
   // CTA: every one is waited for (in order to end; consumers wait for theirs).
-  for (int k = max(0, n - Ti::NS); k < n; ++k) spin(smem_addr(&s->full[k % Ti::NS]), (k / Ti::NS) & 1);
+  for (int k = max(0, n - Ti::NS); k < n; ++k) ok = spin(smem_addr(&s->full[k % Ti::NS]), (k / Ti::NS) & 1) && ok;
+  if (!ok && p.status) *p.status = -5;  // WKV_ERR_TIMEOUT
 }
 
 // MMAs, in the order that the head of this file explains; one whole warp.
@@ -649,6 +650,9 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
   auto tile = [&](const Place<Ti::NS> &t) { return sm + Ti::RING + t.slot * Ti::SLOT; };
   Place<Ti::NS> place;
   bool ok = true;
+  struct {
+    int scores, keys, states, outputs, tiles;
+  } done = {};  // commits to each of the barriers; tiles are freed in the ring's order
 #pragma unroll 1
   for (int it = 0; it < ch.n; ++it) {
     const uint32_t ph = it & 1;
@@ -669,6 +673,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
         mma_commit(smem_addr(&s->scores));
       }
       __syncwarp();
+      ++done.scores;
       if (!(ok = wait_warp(s->r_ready, ph, s, p.status))) break;
     }
     if (!(ok = loaded(nc))) break;
@@ -689,6 +694,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
           if (k == 0) mma_commit(smem_addr(&s->w_free));
         }
         __syncwarp();
+        if (k == 0) ++done.keys;
       }
       if (OUT && k == 0) {
         if (!TWO && it > 0 && !(ok = wait_warp(s->o_free, ph ^ 1u, s, p.status))) break;
@@ -701,15 +707,19 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
           mma_commit(smem_addr(&s->empty[na.slot]));
         }
         __syncwarp();
+        ++done.tiles;
       }
     }
     if (!ok) break;
+    const bool state_done = n_terms > 0 && (OUT || it + 1 == ch.n);
     if (elect_one()) {
       // b is free once its scores are formed and its keys read, or multiplied
       mma_commit(smem_addr(&s->empty[nb.slot]));
-      if (n_terms > 0 && (OUT || it + 1 == ch.n)) mma_commit(smem_addr(&s->state));
+      if (state_done) mma_commit(smem_addr(&s->state));
     }
     __syncwarp();
+    ++done.tiles;
+    done.states += state_done;
     if (OUT) {
       if (!(ok = wait_warp(s->p_ready, ph, s, p.status))) break;
       tc_after_sync();
@@ -725,11 +735,26 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
       mma_commit(smem_addr(&s->empty[nc.slot]));
     }
     __syncwarp();
+    ++done.tiles;
+    done.outputs += OUT;
   }
-  // MMAs in flight read shared memory and write tensor memory: they end before the CTA does
-  if (elect_one()) mma_commit(smem_addr(&s->drain));
-  __syncwarp();
-  if (elect_one()) spin(smem_addr(&s->drain), 0);
+  // Nothing may be under way when the CTA ends.  MMAs in flight read shared
+  // memory and write tensor memory, and a commit arrives on a barrier in shared
+  // memory, which is the SM's next CTA's by then: an arrival too many there ends
+  // a phase early.  So the last arrival of every barrier that MMAs complete is
+  // waited for here, whether or not a role waits for it too.
+  if (elect_one()) {
+    mma_commit(smem_addr(&s->drain));
+    bool ended = spin(smem_addr(&s->drain), 0);
+    auto last_of = [&](uint64_t &bar, int n) { ended = (n == 0 || spin(smem_addr(&bar), (n - 1) & 1)) && ended; };
+    last_of(s->scores, done.scores);
+    last_of(s->w_free, done.keys);
+    last_of(s->state, done.states);
+    last_of(s->o_done, done.outputs);
+    for (int k = max(0, done.tiles - Ti::NS); k < done.tiles; ++k)
+      ended = spin(smem_addr(&s->empty[k % Ti::NS]), (k / Ti::NS) & 1) && ended;
+    if (!ended && p.status) *p.status = -5;  // WKV_ERR_TIMEOUT
+  }
 }
 
 struct Maps {
