@@ -54,6 +54,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "wkv.h"
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -158,8 +160,14 @@ int linattn_backward_saved(int64_t BH, int64_t N, int D, int M, const void *q, c
  *   uninitialised; nothing in it outlives the call.  Its size may be 0 (ws is
  *   then ignored).  Calls that may run at the same time need one each.
  * - status: a device int32 (or NULL), zeroed by its owner; a bounded wait
- *   that gave up stores WKV_ERR_TIMEOUT there (that call's results are then
- *   invalid).  Any number of calls may share it.
+ *   that gave up (about one second, or the options' spin_limit) stores
+ *   WKV_ERR_TIMEOUT there (that call's results are then invalid).  Any number
+ *   of calls may share it.
+ * - The _ex forms take wkv_options (wkv.h; NULL: the defaults).  kernel has to
+ *   be WKV_KERNEL_AUTO; spin_limit bounds the waits of the tensor-core
+ *   kernels, in microseconds (in steps of about 4); test_hold_first_chunk
+ *   holds an arrival back in the first block of each of their launches, so
+ *   that its waits run out.  The recurrence waits for nothing.
  * - Results are bit-reproducible.
  */
 typedef struct {
@@ -188,6 +196,10 @@ int linattn_decay_forward(int64_t B, int64_t T, int64_t H, int D, int M, int dty
                           const linattn_view *k, const linattn_view *v, const float *log_decay, float scale,
                           const int32_t *lengths, const float *state_in, const linattn_view *out, float *state_out,
                           void *ws, size_t ws_bytes, int32_t *status, void *stream);
+int linattn_decay_forward_ex(int64_t B, int64_t T, int64_t H, int D, int M, int dtype, const linattn_view *q,
+                             const linattn_view *k, const linattn_view *v, const float *log_decay, float scale,
+                             const int32_t *lengths, const float *state_in, const linattn_view *out, float *state_out,
+                             void *ws, size_t ws_bytes, int32_t *status, void *stream, const wkv_options *opt);
 
 /*
  * Gradients of a scalar loss L given grad_out = dL/dout and, optionally,
@@ -207,6 +219,12 @@ int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, int M, int dt
                            const float *grad_state_out, const linattn_view *grad_q, const linattn_view *grad_k,
                            const linattn_view *grad_v, float *grad_state_in, void *ws, size_t ws_bytes,
                            int32_t *status, void *stream);
+int linattn_decay_backward_ex(int64_t B, int64_t T, int64_t H, int D, int M, int dtype, const linattn_view *q,
+                              const linattn_view *k, const linattn_view *v, const float *log_decay, float scale,
+                              const int32_t *lengths, const float *state_in, const linattn_view *grad_out,
+                              const float *grad_state_out, const linattn_view *grad_q, const linattn_view *grad_k,
+                              const linattn_view *grad_v, float *grad_state_in, void *ws, size_t ws_bytes,
+                              int32_t *status, void *stream, const wkv_options *opt);
 
 /*
  * One token for each of N sequences: state_out = lam state_in + k v^T,

@@ -28,7 +28,7 @@ EXPORTS = (
     # include/linattn.h
     "linattn_workspace_size", "linattn_forward", "linattn_backward", "linattn_backward_saved",
     "linattn_decay_workspace_size", "linattn_decay_forward", "linattn_decay_backward", "linattn_decay_step",
-    "linattn_rotary",
+    "linattn_decay_forward_ex", "linattn_decay_backward_ex", "linattn_rotary",
 )
 
 
@@ -96,6 +96,8 @@ _SIGS = {
     "linattn_rotary": (_int, [_i64, _i64, _int, _int, _int, _i64, _view, _i64, _view, _p, _int, _i64, _p, _f32, _int,
                               _int, _view, _view, _p]),
 }
+for _name in ("linattn_decay_forward", "linattn_decay_backward"):
+    _SIGS[_name + "_ex"] = (_int, _SIGS[_name][1] + [_opt])
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
     _fn.restype = _res
@@ -287,11 +289,25 @@ def linattn_decay_forward(B, T, H, D, M, dtype, q, k, v, log_decay, scale, lengt
                                      _v(out), state_out, ws, ws_bytes, status, stream)
 
 
+def linattn_decay_forward_ex(B, T, H, D, M, dtype, q, k, v, log_decay, scale, lengths, state_in, out, state_out, ws,
+                             ws_bytes, status, stream, opt=None):
+    return lib.linattn_decay_forward_ex(B, T, H, D, M, dtype, _v(q), _v(k), _v(v), log_decay, scale, lengths, state_in,
+                                        _v(out), state_out, ws, ws_bytes, status, stream, _opts(opt))
+
+
 def linattn_decay_backward(B, T, H, D, M, dtype, q, k, v, log_decay, scale, lengths, state_in, grad_out,
                            grad_state_out, grad_q, grad_k, grad_v, grad_state_in, ws, ws_bytes, status, stream):
     return lib.linattn_decay_backward(B, T, H, D, M, dtype, _v(q), _v(k), _v(v), log_decay, scale, lengths, state_in,
                                       _v(grad_out), grad_state_out, _v(grad_q), _v(grad_k), _v(grad_v),
                                       grad_state_in, ws, ws_bytes, status, stream)
+
+
+def linattn_decay_backward_ex(B, T, H, D, M, dtype, q, k, v, log_decay, scale, lengths, state_in, grad_out,
+                              grad_state_out, grad_q, grad_k, grad_v, grad_state_in, ws, ws_bytes, status, stream,
+                              opt=None):
+    return lib.linattn_decay_backward_ex(B, T, H, D, M, dtype, _v(q), _v(k), _v(v), log_decay, scale, lengths,
+                                         state_in, _v(grad_out), grad_state_out, _v(grad_q), _v(grad_k), _v(grad_v),
+                                         grad_state_in, ws, ws_bytes, status, stream, _opts(opt))
 
 
 def linattn_decay_step(N, H, D, M, dtype, q, k, v, log_decay, scale, state_in, out, state_out, stream):

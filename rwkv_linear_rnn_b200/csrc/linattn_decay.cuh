@@ -54,7 +54,14 @@ struct Pass {
   int nseg;                // segments per head
   int64_t seg_len;         // positions per segment
   float *seg;              // [B * H][nseg][X][Y] float32: segment sums, then the states at the segments' starts
-  int32_t *status;
+};
+
+// Bounded waits inside a block: a role's wait gives up after `tries` (and a
+// block that has to end with its loads or products under way after kTries).
+struct Waits {
+  int32_t *status;  // receives WKV_ERR_TIMEOUT; or null
+  uint32_t tries;
+  int hold;  // test: the first block's waits run out
 };
 
 // Passes of one call that are launched together (blockIdx.y): they have the
@@ -62,6 +69,7 @@ struct Pass {
 struct Group {
   Pass p[3];
   int n;
+  Waits w;
 };
 
 // Positions of row b.
@@ -127,6 +135,8 @@ inline bool tc_one_class(int D, int M) { return (D <= 64) == (M <= 64); }
 int64_t tc_segments(int64_t BH, int64_t T, int X, int Y, int npass, int sms);
 int64_t tc_segment_len(int64_t T, int64_t nseg);
 cudaError_t launch_tc(const Group &g, bool sums_only, int sms, cudaStream_t st);
+// Tries that take about `us` microseconds when nothing arrives; the default for us <= 0.
+uint32_t tc_tries(int64_t us);
 struct StepArgs {
   int64_t N, H;
   int D, M;

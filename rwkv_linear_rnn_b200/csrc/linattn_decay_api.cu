@@ -114,18 +114,27 @@ cudaError_t run_group(Group &g, const Dims &d, bool tc, void *ws, cudaStream_t s
   }
   return e == cudaSuccess ? launch(false) : e;
 }
-cudaError_t run_passes(const Pass *p, int n, const Dims &d, void *ws, cudaStream_t st) {
+cudaError_t run_passes(const Pass *p, int n, const Dims &d, const Waits &w, void *ws, cudaStream_t st) {
   bool tc = uses_tc(d);
   for (int i = 0; i < n; ++i) tc = tc && tc_fits(p[i]);
   const bool one = tc ? tc_one_class(d.D, d.M) : rec_class(d.D) == rec_class(d.M);
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < n && e == cudaSuccess;) {
     Group g{};
+    g.w = w;
     const int X = p[i].X;
     while (i < n && (one || p[i].X == X)) g.p[g.n++] = p[i++];
     e = run_group(g, d, tc, ws, st);
   }
   return e;
+}
+
+// Options: AUTO is the only choice of kernel.
+int check_options(const wkv_options *opt) {
+  return opt && (opt->kernel != WKV_KERNEL_AUTO || opt->spin_limit < 0) ? WKV_ERR_INVALID_ARG : WKV_OK;
+}
+Waits waits(const wkv_options *opt, int32_t *status) {
+  return Waits{status, tc_tries(opt ? opt->spin_limit : 0), opt ? opt->test_hold_first_chunk : 0};
 }
 
 // T = 0, or no work at all: the state goes through.
@@ -146,8 +155,17 @@ extern "C" int linattn_decay_forward(int64_t B, int64_t T, int64_t H, int D, int
                                      const linattn_view *k, const linattn_view *v, const float *log_decay, float scale,
                                      const int32_t *lengths, const float *state_in, const linattn_view *out,
                                      float *state_out, void *ws, size_t ws_bytes, int32_t *status, void *stream) {
+  return linattn_decay_forward_ex(B, T, H, D, M, dtype, q, k, v, log_decay, scale, lengths, state_in, out, state_out, ws,
+                                  ws_bytes, status, stream, nullptr);
+}
+
+extern "C" int linattn_decay_forward_ex(int64_t B, int64_t T, int64_t H, int D, int M, int dtype,
+                                        const linattn_view *q, const linattn_view *k, const linattn_view *v,
+                                        const float *log_decay, float scale, const int32_t *lengths,
+                                        const float *state_in, const linattn_view *out, float *state_out, void *ws,
+                                        size_t ws_bytes, int32_t *status, void *stream, const wkv_options *opt) {
   const Dims d{B, T, H, D, M, dtype};
-  int rc = check_dims(d);
+  int rc = first_of({check_dims(d), check_options(opt)});
   if (rc != WKV_OK) return rc;
   if (!log_decay) return WKV_ERR_INVALID_ARG;
   if (T > 0) {  // empty tensors may be null
@@ -168,8 +186,8 @@ extern "C" int linattn_decay_forward(int64_t B, int64_t T, int64_t H, int D, int
   p.B = B, p.T = T, p.H = H, p.X = D, p.Y = M;
   p.a = view(q), p.b = view(k), p.c = view(v), p.o = view(out);
   p.log_decay = log_decay, p.lengths = lengths, p.s_in = state_in, p.s_out = state_out;
-  p.si = scale, p.sk = 1.f, p.status = status;
-  return cuda_status(run_passes(&p, 1, d, ws, st));
+  p.si = scale, p.sk = 1.f;
+  return cuda_status(run_passes(&p, 1, d, waits(opt, status), ws, st));
 }
 
 extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, int M, int dtype, const linattn_view *q,
@@ -179,8 +197,21 @@ extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, in
                                       const linattn_view *grad_q, const linattn_view *grad_k,
                                       const linattn_view *grad_v, float *grad_state_in, void *ws, size_t ws_bytes,
                                       int32_t *status, void *stream) {
+  return linattn_decay_backward_ex(B, T, H, D, M, dtype, q, k, v, log_decay, scale, lengths, state_in, grad_out,
+                                   grad_state_out, grad_q, grad_k, grad_v, grad_state_in, ws, ws_bytes, status, stream,
+                                   nullptr);
+}
+
+extern "C" int linattn_decay_backward_ex(int64_t B, int64_t T, int64_t H, int D, int M, int dtype,
+                                         const linattn_view *q, const linattn_view *k, const linattn_view *v,
+                                         const float *log_decay, float scale, const int32_t *lengths,
+                                         const float *state_in, const linattn_view *grad_out,
+                                         const float *grad_state_out, const linattn_view *grad_q,
+                                         const linattn_view *grad_k, const linattn_view *grad_v, float *grad_state_in,
+                                         void *ws, size_t ws_bytes, int32_t *status, void *stream,
+                                         const wkv_options *opt) {
   const Dims d{B, T, H, D, M, dtype};
-  int rc = check_dims(d);
+  int rc = first_of({check_dims(d), check_options(opt)});
   if (rc != WKV_OK) return rc;
   if (!log_decay) return WKV_ERR_INVALID_ARG;
   if (T > 0) {
@@ -209,7 +240,7 @@ extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, in
   Pass p[3]{};
   for (Pass &x : p) {
     x.B = B, x.T = T, x.H = H;
-    x.log_decay = log_decay, x.lengths = lengths, x.status = status;
+    x.log_decay = log_decay, x.lengths = lengths;
   }
   // grad_q: forward in time, the state transposed
   p[0].X = M, p[0].Y = D;
@@ -226,7 +257,7 @@ extern "C" int linattn_decay_backward(int64_t B, int64_t T, int64_t H, int D, in
   p[2].a = view(k), p[2].b = view(q), p[2].c = view(grad_out), p[2].o = view(grad_v);
   p[2].s_in = grad_state_out, p[2].s_out = grad_state_in;
   p[2].si = 1.f, p[2].sk = scale, p[2].reverse = 1;
-  return cuda_status(run_passes(p, 3, d, ws, st));
+  return cuda_status(run_passes(p, 3, d, waits(opt, status), ws, st));
 }
 
 extern "C" int linattn_decay_step(int64_t N, int64_t H, int D, int M, int dtype, const linattn_view *q,

@@ -50,6 +50,7 @@
 
 #include <algorithm>
 
+#include "../../include/wkv.h"
 #include "linattn_decay.cuh"
 #include "wkv_tile.cuh"
 
@@ -59,7 +60,10 @@ namespace decay {
 constexpr int kL = 128;                  // positions per chunk
 constexpr uint32_t kHalf = kL * 128;     // bytes of 128 rows of 64 bfloat16
 constexpr int kMostSlots = 8;             // of the ring of tiles
-constexpr uint32_t kTries = 1u << 23;    // bound on any one wait
+// Bound on any one wait: the hardware suspends a try for about kTryUs
+// microseconds when nothing arrives (measured: 3.9), so that kTries are about a second.
+constexpr int64_t kTryUs = 4;
+constexpr uint32_t kTries = 1000000 / kTryUs;
 
 // ------------------------------------------------------------ tcgen05 ---
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t ncols) {
@@ -276,26 +280,28 @@ struct Roles {
   static constexpr int LOAD = TWO ? 2 : KEYS + 4, MMA = LOAD + 1, THREADS = TWO ? 384 : 32 * (MMA + 1);
 };
 
-// Waits for the phase of `addr` with the given parity, in at most kTries tries
-// (each is suspended by the hardware for a while).
-__device__ __forceinline__ bool spin(uint32_t addr, uint32_t parity) {
+// Waits for the phase of the barrier at `addr` with the given parity, in at
+// most `tries` tries (each is suspended by the hardware for a while).
+__device__ __forceinline__ bool spin(uint32_t addr, uint32_t parity, uint32_t tries) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, %3;\n"
       "TRY%=:\n"
       " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE%=;\n"
-      " add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra TRY%=;\n"
+      " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra TRY%=;\n"
       "DONE%=:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(addr), "r"(parity), "n"(kTries)
+      : "r"(addr), "r"(parity), "r"(tries)
       : "memory");
   return ok != 0;
 }
-// The same for a whole warp; a wait that gives up stores WKV_ERR_TIMEOUT and
-// ends its role.
-__device__ __forceinline__ bool wait_warp(uint64_t &bar, uint32_t parity, Bars *, int32_t *status) {
-  const bool ok = __all_sync(~0u, spin(smem_addr(&bar), parity));
-  if (!ok && status) *status = -5;  // WKV_ERR_TIMEOUT
+__device__ __forceinline__ void gave_up(const Waits &w) {
+  if (w.status) *w.status = WKV_ERR_TIMEOUT;
+}
+// The same for a whole warp; a wait that gives up ends its role.
+__device__ __forceinline__ bool wait_warp(uint64_t &bar, uint32_t parity, const Waits &w) {
+  const bool ok = __all_sync(~0u, spin(smem_addr(&bar), parity, w.tries));
+  if (!ok) gave_up(w);
   return ok;
 }
 // One arrival for a whole warp, behind what its lanes have done.
@@ -328,7 +334,7 @@ struct Chunks {
 // State warpgroup: R at the chunk's start -> its bfloat16 copy in shared memory
 // and, decayed, tensor memory again.  A thread is a row of the state.
 template <int XP, int YP, bool OUT, bool TWO>
-__device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, int64_t unit, float g,
+__device__ __forceinline__ void state_role(const Pass &p, const Waits &lim, Bars *s, uint8_t *sm, const Chunks &ch, int64_t unit, float g,
                                            float *result) {
   using Ti = Tiles<XP, YP, OUT, TWO>;
   const int x = threadIdx.x, warp = x >> 5;
@@ -366,7 +372,7 @@ __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, 
     }
 #pragma unroll 1
     for (int it = 0; it < ch.n; ++it) {
-      if (it > 0 && !wait_warp(s->state, (it - 1) & 1, s, p.status)) return;
+      if (it > 0 && !wait_warp(s->state, (it - 1) & 1, lim)) return;
       if (rows) {
         const Decay d = decay_of(g, ch.valid(it));
         const f2 dm = both(d.m);
@@ -396,7 +402,7 @@ __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, 
   }
   if (!result || !rows) return;
   if (ch.n > 0) {
-    if (!wait_warp(s->state, OUT ? (ch.n - 1) & 1 : 0, s, p.status)) return;
+    if (!wait_warp(s->state, OUT ? (ch.n - 1) & 1 : 0, lim)) return;
     tc_after_sync();
   }
 #pragma unroll 1
@@ -420,7 +426,7 @@ __device__ __forceinline__ void state_role(const Pass &p, Bars *s, uint8_t *sm, 
 // Key warpgroup: lam^n b as two bfloat16 terms, the second in b's place once
 // its scores are formed; a thread has a row (position).
 template <int XP, int YP, bool OUT, bool TWO>
-__device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, const Chunks &ch, float g2, bool more) {
+__device__ __forceinline__ void keys_role(const Pass &p, const Waits &lim, Bars *s, uint8_t *sm, const Chunks &ch, float g2, bool more) {
   using Ti = Tiles<XP, YP, OUT, TWO>;
   const int j = threadIdx.x - 32 * Roles<OUT, TWO>::KEYS;
   Place<Ti::NS> place;
@@ -448,9 +454,9 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
     place = c.next();
     const bool wanted = more || it + 1 < ch.n;
     uint8_t *src = sm + Ti::RING + b.slot * Ti::SLOT, *dst = sm + Ti::W;
-    if (wanted && !wait_warp(s->full[b.slot], b.phase, s, p.status)) return;
+    if (wanted && !wait_warp(s->full[b.slot], b.phase, lim)) return;
     if (nv < kL) {  // rows behind the last position may hold anything: 0 x anything has to be 0
-      if (!wait_warp(s->full[c.slot], c.phase, s, p.status)) return;
+      if (!wait_warp(s->full[c.slot], c.phase, lim)) return;
       uint8_t *tc = sm + Ti::RING + c.slot * Ti::SLOT;
       if (j >= nv) {
 #pragma unroll 1
@@ -469,9 +475,9 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
     // second, negated (the products subtract it), what that leaves (exact in
     // bfloat16) plus w2 b, rounded once
     const uint32_t w1 = pack2(w, w), w2 = pack2(w - lo16(w1), w - lo16(w1)), m1 = w1 ^ 0x80008000u, m2 = w2 ^ 0x80008000u;
-    if (it > 0 && !wait_warp(s->w_free, (it - 1) & 1, s, p.status)) return;
+    if (it > 0 && !wait_warp(s->w_free, (it - 1) & 1, lim)) return;
     convert(src, dst, s->w_full[0], [&](uint32_t x) { return mulb(w1, x); });
-    if (OUT && !wait_warp(s->scores, it & 1, s, p.status)) return;
+    if (OUT && !wait_warp(s->scores, it & 1, lim)) return;
     convert(src, src, s->w_full[1], [&](uint32_t x) { return fmab(m2, x, fmab(m1, x, mulb(w1, x))); });
   }
 }
@@ -482,10 +488,12 @@ __device__ __forceinline__ void keys_role(const Pass &p, Bars *s, uint8_t *sm, c
 template <bool TWO>
 struct Scores {
   const Pass &p;
+  const Waits &lim;
   float g2, f;
   int w, lane, half;
   uint32_t tm;
-  __device__ __forceinline__ Scores(const Pass &p, const Bars *s, float g2) : p(p), g2(g2), f(p.si * p.sk) {
+  __device__ __forceinline__ Scores(const Pass &p, const Waits &lim, const Bars *s, float g2)
+      : p(p), lim(lim), g2(g2), f(p.si * p.sk) {
     const int t = threadIdx.x & 255;
     w = (t >> 5) & 3, lane = t & 31, half = TWO ? 0 : t >> 7;
     tm = s->tmem + ((uint32_t)(32 * w) << 16);
@@ -495,7 +503,7 @@ struct Scores {
     const uint32_t causal = p.reverse ? ~0u << lane : (2u << lane) - 1u;  // columns of the diagonal block that count
     const float *tab = p.reverse ? s->up : s->down;
     const int nv = ch.valid(it);
-    if (!wait_warp(s->scores, it & 1, s, p.status)) return false;
+    if (!wait_warp(s->scores, it & 1, lim)) return false;
     tc_after_sync();
     // blocks of 32 columns; the P of two, 16 columns each, lies where the first's
     // scores were, which are read by then (or not needed)
@@ -552,12 +560,14 @@ struct Scores {
 template <int YP, bool TWO>
 struct Outputs {
   const Pass &p;
+  const Waits &lim;
   float g2;
   bool wide;
   uint32_t tm;
   uint16_t *row;  // of position 0
-  __device__ __forceinline__ Outputs(const Pass &p, const Bars *s, int64_t b, int64_t h, float g2, bool wide)
-      : p(p), g2(g2), wide(wide), tm(s->tmem + ((threadIdx.x & 96u) << 16)),
+  __device__ __forceinline__ Outputs(const Pass &p, const Waits &lim, const Bars *s, int64_t b, int64_t h, float g2,
+                                     bool wide)
+      : p(p), lim(lim), g2(g2), wide(wide), tm(s->tmem + ((threadIdx.x & 96u) << 16)),
         row(static_cast<uint16_t *>(const_cast<void *>(p.o.p)) + b * p.o.sb + h * p.o.sh) {}
   __device__ __forceinline__ bool chunk(Bars *s, const Chunks &ch, int it) const {
     constexpr uint32_t O1 = Cols<YP, TWO>::O1, O2 = Cols<YP, TWO>::O2;
@@ -565,7 +575,7 @@ struct Outputs {
     const f2 w = both(i < nv ? p.si * power(g2, p.reverse ? nv - 1 - i : i + 1) : 0.f);
     const int64_t t = (int64_t)ch.start(it) + i;
     uint16_t *dst = row + t * p.o.st;
-    if (!wait_warp(s->o_done, it & 1, s, p.status)) return false;
+    if (!wait_warp(s->o_done, it & 1, lim)) return false;
     tc_after_sync();
     uint32_t o1[16], o2[16], z[8];
     tmem_ld16_nowait(tm + O1, o1);
@@ -608,7 +618,7 @@ struct Outputs {
 // Loads: the tiles of each chunk in the ring's order, each as soon as its slot
 // is free; one whole warp.
 template <int XP, int YP, bool OUT, bool TWO>
-__device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, int b, int h,
+__device__ __forceinline__ void load_role(const Pass &p, const Waits &lim, Bars *s, uint32_t sm, const Chunks &ch, int b, int h,
                                           const CUtensorMap *am, const CUtensorMap *bm, const CUtensorMap *cm) {
   using Ti = Tiles<XP, YP, OUT, TWO>;
   Place<Ti::NS> place;
@@ -620,7 +630,7 @@ __device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, c
 #pragma unroll 1
     for (int k = 0; k < Ti::PER; ++k) {
       const int slot = place.slot;
-      if (n >= Ti::NS && !(ok = wait_warp(s->empty[slot], place.phase ^ 1u, s, p.status))) break;
+      if (n >= Ti::NS && !(ok = wait_warp(s->empty[slot], place.phase ^ 1u, lim))) break;
       const bool is_c = k == Ti::PER - 1;
       const CUtensorMap *m = is_c ? cm : k == Ti::PER - 2 ? bm : am;
       const uint32_t bytes = is_c ? Ti::CT : Ti::BT, dst = sm + Ti::RING + slot * Ti::SLOT, bar = smem_addr(&s->full[slot]);
@@ -635,18 +645,18 @@ __device__ __forceinline__ void load_role(const Pass &p, Bars *s, uint32_t sm, c
   }
   // The loads in flight write shared memory that outlives this warp, not the
   // CTA: every one is waited for (in order to end; consumers wait for theirs).
-  for (int k = max(0, n - Ti::NS); k < n; ++k) ok = spin(smem_addr(&s->full[k % Ti::NS]), (k / Ti::NS) & 1) && ok;
-  if (!ok && p.status) *p.status = -5;  // WKV_ERR_TIMEOUT
+  for (int k = max(0, n - Ti::NS); k < n; ++k) ok = spin(smem_addr(&s->full[k % Ti::NS]), (k / Ti::NS) & 1, kTries) && ok;
+  if (!ok) gave_up(lim);
 }
 
 // MMAs, in the order that the head of this file explains; one whole warp.
 template <int XP, int YP, bool OUT, bool TWO>
-__device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, const Chunks &ch, bool more) {
+__device__ __forceinline__ void mma_role(const Pass &p, const Waits &lim, Bars *s, uint32_t sm, const Chunks &ch, bool more) {
   using Ti = Tiles<XP, YP, OUT, TWO>;
   using Co = Cols<YP, TWO>;
   constexpr uint32_t SCORES = Co::SCORES, O1 = Co::O1, O2 = Co::O2, ST = Co::ST;
   const uint32_t tm = __shfl_sync(~0u, s->tmem, 0);
-  auto loaded = [&](const Place<Ti::NS> &t) { return wait_warp(s->full[t.slot], t.phase, s, p.status); };
+  auto loaded = [&](const Place<Ti::NS> &t) { return wait_warp(s->full[t.slot], t.phase, lim); };
   auto tile = [&](const Place<Ti::NS> &t) { return sm + Ti::RING + t.slot * Ti::SLOT; };
   Place<Ti::NS> place;
   bool ok = true;
@@ -663,7 +673,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
     if (OUT) {
       if (!(ok = loaded(na) && loaded(nb))) break;
       if (TWO && it > 0) {  // the scores' columns hold O1
-        if (!(ok = wait_warp(s->o_free, ph ^ 1u, s, p.status))) break;
+        if (!(ok = wait_warp(s->o_free, ph ^ 1u, lim))) break;
         tc_after_sync();
       }
       if (elect_one()) {
@@ -674,15 +684,15 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
       }
       __syncwarp();
       ++done.scores;
-      if (!(ok = wait_warp(s->r_ready, ph, s, p.status))) break;
+      if (!(ok = wait_warp(s->r_ready, ph, lim))) break;
     }
     if (!(ok = loaded(nc))) break;
-    if (ch.valid(it) < kL && !(ok = wait_warp(s->c_clean, 0, s, p.status))) break;
+    if (ch.valid(it) < kL && !(ok = wait_warp(s->c_clean, 0, lim))) break;
     // the keys' terms, and a R behind the first of them
 #pragma unroll 1
     for (int k = 0; k < max(n_terms, 1); ++k) {
       if (n_terms > 0) {
-        if (!(ok = wait_warp(s->w_full[k], ph, s, p.status))) break;
+        if (!(ok = wait_warp(s->w_full[k], ph, lim))) break;
         tc_after_sync();
         if (elect_one()) {
           const uint32_t dw = mnmajor(k == 0 ? sm + Ti::W : tb, TWO ? 0u : kHalf), dc = mnmajor(tc, kHalf);
@@ -697,7 +707,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
         if (k == 0) ++done.keys;
       }
       if (OUT && k == 0) {
-        if (!TWO && it > 0 && !(ok = wait_warp(s->o_free, ph ^ 1u, s, p.status))) break;
+        if (!TWO && it > 0 && !(ok = wait_warp(s->o_free, ph ^ 1u, lim))) break;
         tc_after_sync();
         if (elect_one()) {
           const uint32_t da = kmajor(ta), dr = mnmajor(sm + Ti::R, XP * 128);
@@ -721,7 +731,7 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
     ++done.tiles;
     done.states += state_done;
     if (OUT) {
-      if (!(ok = wait_warp(s->p_ready, ph, s, p.status))) break;
+      if (!(ok = wait_warp(s->p_ready, ph, lim))) break;
       tc_after_sync();
     }
     if (elect_one()) {
@@ -745,15 +755,15 @@ __device__ __forceinline__ void mma_role(const Pass &p, Bars *s, uint32_t sm, co
   // waited for here, whether or not a role waits for it too.
   if (elect_one()) {
     mma_commit(smem_addr(&s->drain));
-    bool ended = spin(smem_addr(&s->drain), 0);
-    auto last_of = [&](uint64_t &bar, int n) { ended = (n == 0 || spin(smem_addr(&bar), (n - 1) & 1)) && ended; };
+    bool ended = spin(smem_addr(&s->drain), 0, kTries);
+    auto last_of = [&](uint64_t &bar, int n) { ended = (n == 0 || spin(smem_addr(&bar), (n - 1) & 1, kTries)) && ended; };
     last_of(s->scores, done.scores);
     last_of(s->w_free, done.keys);
     last_of(s->state, done.states);
     last_of(s->o_done, done.outputs);
     for (int k = max(0, done.tiles - Ti::NS); k < done.tiles; ++k)
-      ended = spin(smem_addr(&s->empty[k % Ti::NS]), (k / Ti::NS) & 1) && ended;
-    if (!ended && p.status) *p.status = -5;  // WKV_ERR_TIMEOUT
+      ended = spin(smem_addr(&s->empty[k % Ti::NS]), (k / Ti::NS) & 1, kTries) && ended;
+    if (!ended) gave_up(lim);
   }
 }
 
@@ -811,8 +821,12 @@ __global__ void __launch_bounds__(Roles<OUT, TWO>::THREADS, TWO ? 2 : 1) decay_t
     for (int i = 0; i < kMostSlots; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 1);
     for (uint64_t *f : {&bars.scores, &bars.w_free, &bars.state, &bars.o_done, &bars.drain})
       mbar_init(smem_addr(f), 1);
-    for (uint64_t *f : {&bars.w_full[0], &bars.w_full[1], &bars.c_clean}) mbar_init(smem_addr(f), kKeyThreads / 32);
-    mbar_init(smem_addr(&bars.p_ready), Ro::SCORES);
+    // (held: keys and P are waited for, and one arrival too few comes)
+    const int held = blockIdx.x == 0 && group.w.hold ? 1 : 0;
+    mbar_init(smem_addr(&bars.w_full[0]), kKeyThreads / 32 + held);
+    mbar_init(smem_addr(&bars.w_full[1]), kKeyThreads / 32);
+    mbar_init(smem_addr(&bars.c_clean), kKeyThreads / 32);
+    mbar_init(smem_addr(&bars.p_ready), Ro::SCORES + held);
     mbar_init(smem_addr(&bars.o_free), 4);
     mbar_init(smem_addr(&bars.r_ready), Ro::STATE);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -827,27 +841,27 @@ __global__ void __launch_bounds__(Roles<OUT, TWO>::THREADS, TWO ? 2 : 1) decay_t
   __syncthreads();
   tc_after_sync();
   if (warp < Ro::STATE) {
-    state_role<XP, YP, OUT, TWO>(p, &bars, sm, ch, unit, g, result);
+    state_role<XP, YP, OUT, TWO>(p, group.w, &bars, sm, ch, unit, g, result);
   } else if (warp == Ro::LOAD) {
-    load_role<XP, YP, OUT, TWO>(p, &bars, smem_addr(sm), ch, (int)b, (int)h, &am, &bm, &cm);
+    load_role<XP, YP, OUT, TWO>(p, group.w, &bars, smem_addr(sm), ch, (int)b, (int)h, &am, &bm, &cm);
   } else if (warp == Ro::MMA) {
-    mma_role<XP, YP, OUT, TWO>(p, &bars, smem_addr(sm), ch, result != nullptr);
+    mma_role<XP, YP, OUT, TWO>(p, group.w, &bars, smem_addr(sm), ch, result != nullptr);
   } else if (warp >= Ro::KEYS) {
-    keys_role<XP, YP, OUT, TWO>(p, &bars, sm, ch, g2, result != nullptr);
+    keys_role<XP, YP, OUT, TWO>(p, group.w, &bars, sm, ch, g2, result != nullptr);
   } else if constexpr (TWO) {
-    const Scores<TWO> scores(p, &bars, g2);
-    const Outputs<YP, TWO> outputs(p, &bars, b, h, g2, wide != 0);
+    const Scores<TWO> scores(p, group.w, &bars, g2);
+    const Outputs<YP, TWO> outputs(p, group.w, &bars, b, h, g2, wide != 0);
 #pragma unroll 1
     for (int it = 0; it < ch.n; ++it)
       if (!scores.chunk(&bars, ch, it) || !outputs.chunk(&bars, ch, it)) break;
   } else if constexpr (OUT) {
     if (warp < 8) {
-      const Outputs<YP, TWO> outputs(p, &bars, b, h, g2, wide != 0);
+      const Outputs<YP, TWO> outputs(p, group.w, &bars, b, h, g2, wide != 0);
 #pragma unroll 1
       for (int it = 0; it < ch.n; ++it)
         if (!outputs.chunk(&bars, ch, it)) break;
     } else {
-      const Scores<TWO> scores(p, &bars, g2);
+      const Scores<TWO> scores(p, group.w, &bars, g2);
 #pragma unroll 1
       for (int it = 0; it < ch.n; ++it)
         if (!scores.chunk(&bars, ch, it)) break;
@@ -964,6 +978,7 @@ int64_t tc_segments(int64_t BH, int64_t T, int X, int Y, int npass, int sms) {
   }
   return best;
 }
+uint32_t tc_tries(int64_t us) { return us > 0 ? (uint32_t)std::min<int64_t>((us + kTryUs - 1) / kTryUs, 1u << 30) : kTries; }
 int64_t tc_segment_len(int64_t T, int64_t nseg) {
   const int64_t nch = (T + kL - 1) / kL;
   return (nch + nseg - 1) / nseg * kL;
