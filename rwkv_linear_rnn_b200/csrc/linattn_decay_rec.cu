@@ -427,7 +427,8 @@ __device__ __forceinline__ void store_state(const float (&S)[RX][4], float *s, i
 template <typename E, int RX>
 __global__ void __launch_bounds__(32 * kStepWarps, 3) decay_step_kernel(StepArgs s) {
   constexpr int XP = 8 * RX;
-  __shared__ float sq[XP], sk[XP], sv[16 * kStepWarps];
+  __shared__ __align__(16) float sv[16 * kStepWarps];  // read four at a time
+  __shared__ float sq[XP], sk[XP];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int x0 = (lane >> 2) * RX, y0 = 16 * warp + 4 * (lane & 3);
   const int64_t nh = blockIdx.x, n = nh / s.H, h = nh % s.H;
