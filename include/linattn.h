@@ -241,8 +241,9 @@ int linattn_decay_step(int64_t N, int64_t H, int D, int M, int dtype, const lina
  * and k [B, T, Hk, D] are R / 2 pairs, (x_i, x_{i + R/2}) or, if
  * `interleaved`, (x_{2i}, x_{2i+1}); pair i at position p becomes
  *   mscale * (a cos - b sin, a sin + b cos),  angle = p * inv_freq[i]
- * (angles in float64, reduced before they are rounded to float32; products in
- * float32, one rounding at the end).  Elements from R on are copied.
+ * (angles as pairs of float64, reduced before they are rounded to float32, so
+ * that far positions lose nothing; products in float32, one rounding at the
+ * end).  Elements from R on are copied.
  *   inverse    nonzero: rotates back (sin negated), which is also the
  *              gradient of the call with inverse = 0
  *   positions  [B, T] integers of pos_bytes = 4 or 8 bytes, contiguous in T,

@@ -2,9 +2,10 @@
 // include/linattn.h).
 //
 // Pair i of a head at position p turns by the angle p inv_freq[i].  The
-// angle's turns are formed and reduced in float64 (p reaches 2^53 and float32
-// would lose whole radians from about 2^20 on), the remainder goes to
-// sincospi in float32.  Every element is read once and written once, 16 bytes
+// angle's turns are formed and reduced in float64 pairs, each product with the
+// remainder that an FMA gives (Dekker's product; p reaches 2^53, where float64
+// alone is off by a radian, as float32 is from about 2^20 on), and what is left
+// of a turn goes to sincospi in float32.  Every element is read once and written once, 16 bytes
 // at a time when the layout allows: the kernel is bound by HBM.  A block has up
 // to 512 items of one or a few positions, so that a sine and cosine serve all
 // heads of q and k; a thread's four items are on their way before the sines are
@@ -44,6 +45,15 @@ struct Args {
 };
 
 constexpr int kThreads = 128, kItems = 4;
+// 1 / (2 pi) as a float64 and what is left of it.
+constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnLow = -0x1.6b01ec5417056p-57;
+// The part of p f / (2 pi) beyond whole turns, within half a turn of 0.
+__device__ __forceinline__ float part_of_turn(double p, double f) {
+  const double angle = p * f, t = angle * kTurn;
+  const double low = fma(angle, kTurn, -t) + fma(angle, kTurnLow, fma(p, f, -angle) * kTurn);
+  const double r = t - rint(t) + low;
+  return (float)(r - rint(r));
+}
 // e / d for e d < 2^32 with m = ceil(2^32 / d); 0 stands for d = 1.
 __device__ __forceinline__ uint32_t divide(uint32_t e, uint32_t m) { return m ? __umulhi(e, m) : e; }
 
@@ -160,9 +170,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     while (t >= T) t -= T, ++b;
     const int64_t at = b * a.pos_sb + t;
     const double p = a.pos64 ? (double)static_cast<const int64_t *>(a.pos)[at] : (double)static_cast<const int32_t *>(a.pos)[at];
-    const double turns = p * a.inv_freq[e - i * half] * 0.15915494309189533577;  // 1 / (2 pi)
     float sn, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &sn, &c);
+    sincospif(2.f * part_of_turn(p, a.inv_freq[e - i * half]), &sn, &c);
     cs[e] = make_float2(a.mscale * c, a.inverse ? -a.mscale * sn : a.mscale * sn);
   }
   __syncthreads();
