@@ -328,7 +328,8 @@ def _status_ptr(ref, dev):
         torch = _torch()
         if torch.cuda.is_current_stream_capturing():
             return 0
-        t = ref.new_zeros(1, dtype=torch.int32)
+        with torch.inference_mode(False):  # cleared in place, in whatever mode it is read
+            t = torch.zeros(1, dtype=torch.int32, device=ref.device)
         torch.cuda.current_stream(dev).synchronize()  # zeroed before any other stream's call stores to it
         known = _decay_status.setdefault(dev, (t, t.data_ptr()))  # the first of several threads' stays
     return known[1]
