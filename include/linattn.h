@@ -181,6 +181,14 @@ typedef struct {
 size_t linattn_decay_workspace_size(int op, int64_t B, int64_t T, int64_t H, int D, int M, int dtype);
 
 /*
+ * A status word of the current device for `status`: one int32, zero at first,
+ * that lives as long as the library.  It may be asked for while a stream
+ * captures, and captured calls may be given it.  Returns WKV_OK,
+ * WKV_ERR_INVALID_ARG (null) or WKV_ERR_CUDA.
+ */
+int linattn_decay_status_word(int32_t **word);
+
+/*
  * Forward over whole sequences.
  *   q, k, v    views, read
  *   state_in   nullable: the state before position 0

@@ -319,36 +319,41 @@ def _scope(t, stream):
 _decay_status = {}  # device index -> (the device's status word, its address)
 
 
-def _status_ptr(ref, dev):
-    """The status word of ``ref``'s device.  It is shared by every call (kernels only ever
-    store an error there) and lives as long as the process; a call captured
-    into a graph before any eager one goes without."""
+class _Word:
+    """The int32 at a device address, for torch.as_tensor."""
+
+    def __init__(self, address):
+        self.__cuda_array_interface__ = dict(shape=(1,), typestr="<i4", data=(address, False), strides=None, version=2)
+
+
+def _status_ptr(dev):
+    """Address of the status word of ``dev``, the current device.  It is shared by every call (kernels only
+    ever store an error there), captured ones too, and belongs to the library."""
     known = _decay_status.get(dev)
     if known is None:
         torch = _torch()
+        address = _abi().linattn_decay_status_word()
         if torch.cuda.is_current_stream_capturing():
-            return 0
+            return address  # the tensor can wait
         with torch.inference_mode(False):  # cleared in place, in whatever mode it is read
-            t = torch.zeros(1, dtype=torch.int32, device=ref.device)
-        torch.cuda.current_stream(dev).synchronize()  # zeroed before any other stream's call stores to it
-        known = _decay_status.setdefault(dev, (t, t.data_ptr()))  # the first of several threads' stays
+            t = torch.as_tensor(_Word(address), device=f"cuda:{dev}")
+        known = _decay_status.setdefault(dev, (t, address))
     return known[1]
 
 
 def linattn_decay_status(device=None):
-    """Device-side status of the ``linattn_decay_*`` calls made so far (0, or
+    """Device-side status of the ``linattn_decay_*`` calls made so far, replayed ones among them (0, or
     WKV_ERR_TIMEOUT if a bounded wait gave up); waits for the device and clears it."""
     torch = _torch()
     device = torch.device("cuda" if device is None else device)
     index = torch.cuda.current_device() if device.index is None else device.index
-    known = _decay_status.get(index)
-    if known is None:
-        return 0
-    t = known[0]
-    torch.cuda.synchronize(index)
-    rc = int(t.item())
-    if rc:
-        t.zero_()
+    with torch.cuda.device(index):
+        _status_ptr(index)
+        t = _decay_status[index][0]
+        torch.cuda.synchronize(index)
+        rc = int(t.item())
+        if rc:
+            t.zero_()
     return rc
 
 
@@ -442,7 +447,7 @@ def linattn_decay_forward(q, k, v, log_decay, state=None, *, scale=1.0, lengths=
     at = array.array("q", at)
     w, abi = at.buffer_info()[0], _abi()
     rc = abi.linattn_decay_forward_at(B, T, H, D, M, dt, w, w + 32, w + 64, g, scale, n, s_in, w + 96, _ptr(s_out),
-                                      _ptr(ws), need, _status_ptr(q, dev), torch._C._cuda_getCurrentRawStream(dev))
+                                      _ptr(ws), need, _status_ptr(dev), torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         abi.check(rc)
     return out, s_out
@@ -485,7 +490,7 @@ def linattn_decay_backward(q, k, v, log_decay, grad_out, state=None, *, scale=1.
     at = array.array("q", at)
     w, abi = at.buffer_info()[0], _abi()
     rc = abi.linattn_decay_backward_at(B, T, H, D, M, dt, w, w + 32, w + 64, g, scale, n, s_in, w + 96, gs_out, w + 128,
-                                       w + 160, w + 192, _ptr(gs), _ptr(ws), need, _status_ptr(q, dev),
+                                       w + 160, w + 192, _ptr(gs), _ptr(ws), need, _status_ptr(dev),
                                        torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         abi.check(rc)

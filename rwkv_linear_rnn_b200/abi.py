@@ -28,7 +28,8 @@ EXPORTS = (
     # include/linattn.h
     "linattn_workspace_size", "linattn_forward", "linattn_backward", "linattn_backward_saved",
     "linattn_decay_workspace_size", "linattn_decay_forward", "linattn_decay_backward", "linattn_decay_step",
-    "linattn_decay_forward_ex", "linattn_decay_backward_ex", "linattn_rotary",
+    "linattn_decay_forward_ex", "linattn_decay_backward_ex", "linattn_decay_status_word",
+    "linattn_rotary",
 )
 
 
@@ -96,6 +97,7 @@ _SIGS = {
     "linattn_rotary": (_int, [_i64, _i64, _int, _int, _int, _i64, _view, _i64, _view, _p, _int, _i64, _p, _f32, _int,
                               _int, _view, _view, _p]),
 }
+_SIGS["linattn_decay_status_word"] = (_int, [ctypes.POINTER(_p)])
 for _name in ("linattn_decay_forward", "linattn_decay_backward"):
     _SIGS[_name + "_ex"] = (_int, _SIGS[_name][1] + [_opt])
 for _name, (_res, _args) in _SIGS.items():
@@ -281,6 +283,13 @@ def _v(view):
 
 def linattn_decay_workspace_size(op, B, T, H, D, M, dtype):
     return lib.linattn_decay_workspace_size(op, B, T, H, D, M, dtype)
+
+
+def linattn_decay_status_word():
+    """Address of the current device's status word."""
+    word = _p()
+    check(lib.linattn_decay_status_word(ctypes.byref(word)))
+    return word.value
 
 
 def linattn_decay_forward(B, T, H, D, M, dtype, q, k, v, log_decay, scale, lengths, state_in, out, state_out, ws,

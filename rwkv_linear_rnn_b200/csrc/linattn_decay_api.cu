@@ -137,6 +137,9 @@ Waits waits(const wkv_options *opt, int32_t *status) {
   return Waits{status, tc_tries(opt ? opt->spin_limit : 0), opt ? opt->test_hold_first_chunk : 0};
 }
 
+// linattn_decay_status_word's, one on each device.
+__device__ int32_t status_word;
+
 // T = 0, or no work at all: the state goes through.
 int pass_state_through(const Dims &d, const float *in, float *out, cudaStream_t st) {
   if (!out || in == out) return WKV_OK;
@@ -149,6 +152,19 @@ extern "C" size_t linattn_decay_workspace_size(int op, int64_t B, int64_t T, int
   const Dims d{B, T, H, D, M, dtype};
   if ((op != LINATTN_OP_FORWARD && op != LINATTN_OP_BACKWARD) || check_dims(d) != WKV_OK) return 0;
   return workspace(op, d);
+}
+
+extern "C" int linattn_decay_status_word(int32_t **word) {
+  if (!word) return WKV_ERR_INVALID_ARG;
+  // The first use of a module loads it, which a thread that captures may only do in the relaxed mode.
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return cuda_status(e);
+  void *p = nullptr;
+  e = cudaGetSymbolAddress(&p, status_word);
+  const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+  *word = static_cast<int32_t *>(p);
+  return cuda_status(e == cudaSuccess ? back : e);
 }
 
 extern "C" int linattn_decay_forward(int64_t B, int64_t T, int64_t H, int D, int M, int dtype, const linattn_view *q,

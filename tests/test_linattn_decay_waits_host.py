@@ -13,3 +13,7 @@ def test_options(W, options, code):  # noqa: F811
     assert W.abi.linattn_decay_forward_ex(1, 0, 2, 32, 32, 0, *v[:3], F, 1.0, 0, 0, v[3], 0, 0, 0, 0, 0, opt) == code
     assert W.abi.linattn_decay_backward_ex(1, 0, 2, 32, 32, 0, *v[:3], F, 1.0, 0, 0, v[3], 0, *v[4:], 0, 0, 0, 0, 0,
                                            opt) == code
+
+
+def test_status_word_needs_a_place(W):  # noqa: F811
+    assert W.abi.lib.linattn_decay_status_word(None) == INVALID
