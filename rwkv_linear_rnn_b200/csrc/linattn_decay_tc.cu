@@ -499,7 +499,7 @@ struct Scores {
     tm = s->tmem + ((uint32_t)(32 * w) << 16);
   }
   __device__ __forceinline__ bool chunk(Bars *s, const Chunks &ch, int it) const {
-    const bool moderate = g2 * 31.f > -100.f;
+    const bool moderate = g2 * 31.f > -100.f && fabsf(f) < 0x1p27f;  // their product below 2^127
     const uint32_t causal = p.reverse ? ~0u << lane : (2u << lane) - 1u;  // columns of the diagonal block that count
     const float *tab = p.reverse ? s->up : s->down;
     const int nv = ch.valid(it);
@@ -518,8 +518,8 @@ struct Scores {
         uint32_t v[32];
         tmem_ld32_nowait(tm + 32 * cb, v);
         // lam^{|i-j|} as a factor of the row and one of the column; on the
-        // diagonal the row's is up to lam^{-31}, so strong decays take the
-        // product from a table there
+        // diagonal the row's is up to f lam^{-31}, so strong decays and large
+        // scales take the product from a table there
         const int i = 32 * (w - cb) + lane;
         const f2 e = both(f * ex2(g2 * (float)(p.reverse ? -i : i - 31)));
         tmem_wait_ld();
