@@ -548,7 +548,7 @@ class LinattnDecay:
 
     @classmethod
     def apply(cls, q, k, v, log_decay, state=None, lengths=None, scale=1.0, want_state=True):
-        if log_decay.requires_grad:
+        if log_decay.requires_grad and _torch().is_grad_enabled():
             raise ValueError("log_decay is a constant of linattn_decay: it has no gradient (detach it)")
         if cls._fn is None:
             torch = _torch()
