@@ -684,6 +684,8 @@ class Rotary:
 
     @classmethod
     def apply(cls, q, k, positions, inv_freq, mscale=1.0, interleaved=False):
+        if inv_freq.requires_grad and _torch().is_grad_enabled():
+            raise ValueError("inv_freq is a constant of rotary: it has no gradient (detach it)")
         if cls._fn is None:
             torch = _torch()
             from torch.autograd.function import once_differentiable

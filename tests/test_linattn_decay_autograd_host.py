@@ -20,3 +20,16 @@ def test_a_decay_parameter_is_refused_only_where_gradients_are_recorded(W):  # n
                 call(q, q, q, g)
         with pytest.raises(ValueError, match="CUDA device"):
             call(q, q, q, g.detach())
+
+
+def test_frequencies_that_ask_for_a_gradient_are_refused(W):  # noqa: F811
+    """The rotation's frequencies are constants too: no silent missing gradient."""
+    q = torch.zeros(1, 2, 1, 4, requires_grad=True)
+    f = torch.ones(2, dtype=torch.float64, requires_grad=True)
+    pos = torch.arange(2)
+    with pytest.raises(ValueError, match="constant"):
+        W.rotary(q, None, pos, f)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):
+        W.rotary(q, None, pos, f)
+    with pytest.raises(ValueError, match="CUDA device"):
+        W.rotary(q, None, pos, f.detach())
