@@ -402,6 +402,14 @@ def _decay_need(dev, op, B, T, H, D, M, dt):
     return _abi().linattn_decay_workspace_size(op, B, T, H, D, M, dt)
 
 
+def _written(given):
+    """Tells autograd that the library wrote into these of the caller's tensors (None: it had none to give), as
+    torch's own in-place operations do: a graph that saved one refuses its backward."""
+    given = [t for t in given if t is not None]
+    if given:
+        _torch().autograd.graph.increment_version(given)
+
+
 def _scratch(ref, nbytes):
     # per call, from torch's stream-ordered allocator: calls on other streams,
     # in other threads or in captured graphs never share it
@@ -435,6 +443,7 @@ def linattn_decay_forward(q, k, v, log_decay, state=None, *, scale=1.0, lengths=
     _head_view(at, "q", q, dev, dtype, (B, T, H, D))
     _head_view(at, "k", k, dev, dtype, (B, T, H, D))
     _head_view(at, "v", v, dev, dtype, (B, T, H, M))
+    given = out
     if out is None:
         out = q.new_empty((B, T, H, M))
     _head_view(at, "out", out, dev, dtype, (B, T, H, M))
@@ -450,6 +459,7 @@ def linattn_decay_forward(q, k, v, log_decay, state=None, *, scale=1.0, lengths=
                                       _ptr(ws), need, _status_ptr(dev), torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         abi.check(rc)
+    _written((given,))
     return out, s_out
 
 
@@ -474,6 +484,7 @@ def linattn_decay_backward(q, k, v, log_decay, grad_out, state=None, *, scale=1.
     _head_view(at, "k", k, dev, dtype, wide_d)
     _head_view(at, "v", v, dev, dtype, wide_m)
     _head_view(at, "grad_out", grad_out, dev, dtype, wide_m)
+    given = grad_q, grad_k, grad_v
     grad_q = q.new_empty(wide_d) if grad_q is None else grad_q
     grad_k = q.new_empty(wide_d) if grad_k is None else grad_k
     grad_v = q.new_empty(wide_m) if grad_v is None else grad_v
@@ -494,6 +505,7 @@ def linattn_decay_backward(q, k, v, log_decay, grad_out, state=None, *, scale=1.
                                        torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         abi.check(rc)
+    _written(given)
     return grad_q, grad_k, grad_v, gs
 
 
@@ -514,6 +526,7 @@ def linattn_decay_step(q, k, v, log_decay, state, *, scale=1.0, out=None, state_
     _head_view(at, "q", q, dev, dtype, (N, H, D))
     _head_view(at, "k", k, dev, dtype, (N, H, D))
     _head_view(at, "v", v, dev, dtype, (N, H, M))
+    given = out
     if out is None:
         out = q.new_empty((N, H, M))
     _head_view(at, "out", out, dev, dtype, (N, H, M))
@@ -528,6 +541,7 @@ def linattn_decay_step(q, k, v, log_decay, state, *, scale=1.0, out=None, state_
                                    torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         abi.check(rc)
+    _written((state_out, given))
     return out, state_out
 
 
@@ -650,6 +664,7 @@ def linattn_rotary(q, k, positions, inv_freq, *, mscale=1.0, interleaved=False, 
         raise ValueError("inv_freq must be a float64 vector")
     pairs = inv_freq.shape[0]
     f = _plain_ptr("inv_freq", inv_freq, dev, torch.float64, (pairs,))
+    given = out_q, out_k
     at = []
     _head_view(at, "q", q, dev, dtype, shape)
     if out_q is None:
@@ -673,6 +688,7 @@ def linattn_rotary(q, k, positions, inv_freq, *, mscale=1.0, interleaved=False, 
                                w + 96 if Hk else None, torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         abi.check(rc)
+    _written(given)
     return out_q, out_k
 
 
