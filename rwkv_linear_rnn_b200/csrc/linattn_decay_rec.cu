@@ -384,11 +384,10 @@ __device__ __forceinline__ int reduced_column(int lane) {
   return 4 * (lane & 3) + ((lane & 16) ? 2 : 0) + ((lane & 8) ? 1 : 0);
 }
 
-// A lane's RX x 4 part of a state of X x Y at `s` (or Y x X, transposed).
+// A lane's RX x 4 part of a state of X x Y at `s`.
 template <int RX>
-__device__ __forceinline__ void load_state(float (&S)[RX][4], const float *s, int X, int Y, int x0, int y0,
-                                           bool transposed) {
-  const bool vec = !transposed && (Y & 3) == 0;
+__device__ __forceinline__ void load_state(float (&S)[RX][4], const float *s, int X, int Y, int x0, int y0) {
+  const bool vec = (Y & 3) == 0;
 #pragma unroll
   for (int r = 0; r < RX; ++r) {
     const int x = x0 + r;
@@ -398,7 +397,7 @@ __device__ __forceinline__ void load_state(float (&S)[RX][4], const float *s, in
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        S[r][q] = (x < X && y0 + q < Y) ? s[transposed ? (int64_t)(y0 + q) * X + x : (int64_t)x * Y + y0 + q] : 0.f;
+        S[r][q] = (x < X && y0 + q < Y) ? s[(int64_t)x * Y + y0 + q] : 0.f;
     }
   }
 }
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(32 * kStepWarps, 3) decay_step_kernel(StepArgs
   const int64_t nh = blockIdx.x, n = nh / s.H, h = nh % s.H;
   const int64_t DM = (int64_t)s.D * s.M;
   float S[RX][4];
-  load_state<RX>(S, s.s_in + nh * DM, s.D, s.M, x0, y0, false);
+  load_state<RX>(S, s.s_in + nh * DM, s.D, s.M, x0, y0);
   const Decay lam = decay_of(s.log_decay[h], 1);
   for (int x = threadIdx.x; x < XP; x += blockDim.x) {
     sq[x] = x < s.D ? load1<E>(s.q.p, n * s.q.sb + h * s.q.sh + x) : 0.f;
