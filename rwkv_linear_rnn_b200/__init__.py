@@ -553,6 +553,15 @@ def _rows(t):
     return t.contiguous()
 
 
+def _state(t):
+    """A state or its gradient as the library takes it: slices that are not contiguous, or not 16-byte aligned
+    (of odd sizes, or a gradient cut from a larger one), are copied."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class LinattnDecay:
     """torch.autograd.Function wrapper: (out, state_out) = LinattnDecay.apply(q, k, v, log_decay, state,
     lengths, scale).  Gradients reach state through both out and state_out, so a sequence split across
@@ -573,7 +582,7 @@ class LinattnDecay:
                 def forward(ctx, q, k, v, log_decay, state, lengths, scale, want_state):
                     ctx.set_materialize_grads(False)
                     q, k, v = _rows(q), _rows(k), _rows(v)
-                    state = None if state is None else state.contiguous()
+                    state = _state(state)
                     out, s_out = linattn_decay_forward(q, k, v, log_decay, state, scale=scale, lengths=lengths,
                                                        want_state=want_state)
                     ctx.save_for_backward(q, k, v, log_decay, state, lengths)
@@ -587,7 +596,7 @@ class LinattnDecay:
                     go = torch.zeros_like(v) if go is None else go
                     gq, gk, gv, gst = linattn_decay_backward(
                         q, k, v, log_decay, _rows(go), state, scale=ctx.scale, lengths=lengths,
-                        grad_state_out=None if gs is None else gs.contiguous(),
+                        grad_state_out=_state(gs),
                         want_grad_state=state is not None and ctx.needs_input_grad[4])
                     return gq, gk, gv, None, gst, None, None, None
 

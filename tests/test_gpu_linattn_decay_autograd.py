@@ -74,3 +74,27 @@ def test_evaluating_with_a_decay_parameter(graph):
     with torch.no_grad():
         out = W.linattn_decay(graph["q"], graph["k"], graph["v"], decay, graph["state"])
     assert torch.equal(out, graph["out"].detach())
+
+
+@pytest.mark.parametrize("D,M", [(3, 5), (7, 1), (64, 64)])
+def test_states_that_are_slices_off_16_bytes(D, M):
+    """States of odd sizes cut from a larger tensor, and their gradients cut from a larger one by cat's backward."""
+    q, k = (x.requires_grad_() for x in tensors(2, 1, 9, 1, D))
+    v = torch.randn(1, 9, 1, M, device="cuda", requires_grad=True)
+    g = torch.tensor([-0.1], device="cuda")
+    pool = torch.randn(3, 1, D, M, device="cuda", requires_grad=True)
+    weight = torch.randn(2, 1, D, M, device="cuda")
+
+    def loss(state):
+        outs = [W.linattn_decay_state(q, k, v, g, state(i)) for i in (1, 2)]
+        s = torch.cat([s for _, s in outs])
+        return sum(o.sum() for o, _ in outs) + (s * weight).sum()
+
+    def grads(state):
+        for t in (q, k, v, pool):
+            t.grad = None
+        loss(state).backward()
+        return [t.grad.clone() for t in (q, k, v, pool)]
+
+    for a, b in zip(grads(lambda i: pool[i:i + 1]), grads(lambda i: pool[i:i + 1].clone())):
+        assert torch.equal(a, b) and bool(a.abs().sum() > 0)
