@@ -459,7 +459,8 @@ def linattn_decay_forward(q, k, v, log_decay, state=None, *, scale=1.0, lengths=
                                       _ptr(ws), need, _status_ptr(dev), torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         abi.check(rc)
-    _written((given,))
+    if given is not None:
+        _written((given,))
     return out, s_out
 
 
@@ -541,7 +542,7 @@ def linattn_decay_step(q, k, v, log_decay, state, *, scale=1.0, out=None, state_
                                    torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         abi.check(rc)
-    _written((state_out, given))
+    torch.autograd.graph.increment_version(state_out if given is None else (state_out, given))  # as _written
     return out, state_out
 
 
