@@ -978,7 +978,7 @@ int64_t tc_segments(int64_t BH, int64_t T, int X, int Y, int npass, int sms) {
   }
   return best;
 }
-uint32_t tc_tries(int64_t us) { return us > 0 ? (uint32_t)std::min<int64_t>((us + kTryUs - 1) / kTryUs, 1u << 30) : kTries; }
+uint32_t tc_tries(int64_t us) { return us > 0 ? (uint32_t)std::min<int64_t>((us - 1) / kTryUs + 1, 1u << 30) : kTries; }
 int64_t tc_segment_len(int64_t T, int64_t nseg) {
   const int64_t nch = (T + kL - 1) / kL;
   return (nch + nseg - 1) / nseg * kL;

@@ -91,3 +91,20 @@ def test_a_wait_that_runs_out_is_reported_and_the_context_survives(B, T, H, D, M
             assert status.item() == 0
             assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert W.linattn_decay_status() == 0
+
+
+@pytest.mark.parametrize("spin_limit", [1, 1 << 31, (1 << 63) - 1])
+def test_the_smallest_and_the_largest_limit(spin_limit):
+    """The largest is bounded all the same and does not wrap round to none; the smallest may give up, and says so."""
+    q, k, v, g, _ = inputs(5, 1, 300, 2, 64, 64)
+    ref, _ = W.linattn_decay_forward(q, k, v, g)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    need = W.linattn_decay_workspace_size(0, 1, 300, 2, 64, 64, W.WKV_BF16)
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(ref)
+    assert 0 == abi.linattn_decay_forward_ex(
+        1, 300, 2, 64, 64, W.WKV_BF16, view(q), view(k), view(v), g.data_ptr(), 1.0, 0, 0, view(out), 0, ws.data_ptr(), need,
+        status.data_ptr(), torch.cuda.current_stream().cuda_stream, abi.Options(spin_limit=spin_limit))
+    if spin_limit > 1:
+        assert status.item() == 0
+    assert status.item() == WKV_ERR_TIMEOUT or torch.equal(out, ref)
