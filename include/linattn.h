@@ -139,12 +139,22 @@ int linattn_backward_saved(int64_t BH, int64_t N, int D, int M, const void *q, c
  *   linattn_view: a device pointer and the strides, in elements, of batch,
  *   time and head; the feature index is contiguous.  Strides are >= 0; those
  *   of an output must not make it overlap itself.  So [B, H, T, D] tensors
- *   and slices of a fused projection need no copy.
+ *   and slices of a fused projection need no copy.  An output shares no element
+ *   with an input or another output (checked is that no two start at the same
+ *   address).
  * - Head sizes: 1 <= D, M <= 128.  The tensor-core kernels run when dtype is
  *   WKV_BF16, D and M are multiples of 8, pointers are 16-byte aligned,
  *   strides are multiples of 8 elements, > 0 and below 2^39, and T is above
- *   32; other calls run the recurrence on the CUDA cores.
+ *   32; other calls run the recurrence on the CUDA cores.  So keys or values
+ *   that heads share through a stride of 0 run the recurrence: over more than a
+ *   few positions a copy for each head is faster (8 x 1024 x 12 heads of 64,
+ *   forward 270 us against 48 with the copies, gradients 940 against 63).
+ * - A caller that wants float32 products of bfloat16 tensors converts them:
+ *   WKV_F32 runs the recurrence (states to 3e-7 instead of 4e-6; 8 x 1024 x 12
+ *   heads of 64, 86 us instead of 22).
  * - Sizes: B, H >= 1, B * H < 2^24 (N * H < 2^31 for the step), 0 <= T < 2^31.
+ * - The recurrence holds up to 2^16 times its state and products, so values
+ *   whose sums stay below 2^111 are safe from overflow.
  * - log_decay [H] float32, at most 0 (minus infinity allowed: lam = 0).  It is
  *   a constant: no call returns a gradient for it.
  * - lengths [B] int32 on the device, or NULL (every row has T positions): row

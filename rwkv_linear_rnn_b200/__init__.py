@@ -428,7 +428,8 @@ def linattn_decay_forward(q, k, v, log_decay, state=None, *, scale=1.0, lengths=
     out_t = scale * q_t^T S_t with S_t = e^{log_decay[h]} S_{t-1} + k_t v_t^T, for q, k [B, T, H, D] and
     v [B, T, H, M] (float32 or bfloat16; any strides with a contiguous last dimension), log_decay [H]
     float32 <= 0, the state before position 0 (``state`` [B, H, D, M] float32, or empty) and each row's
-    number of positions (``lengths`` [B] int32, or T for all; out is zero behind them).  Returns
+    number of positions (``lengths`` [B] int32, or T for all; out is zero behind them).  Keys and values that
+    heads share are faster as copies than expanded (strides of 0 keep off the tensor cores).  Returns
     (out [B, T, H, M], the state after each row's last position or None)."""
     torch = _torch()
     dev, current = _on_device(q)

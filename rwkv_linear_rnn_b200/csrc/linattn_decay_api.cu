@@ -71,7 +71,14 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t seg_bytes(const Dims &d, int64_t nseg) { return nseg > 1 ? up256(sizeof(float) * d.B * d.H * nseg * d.D * d.M) : 0; }
 
 // Whether a call's passes run on the tensor cores, as far as its sizes say.
-// Up to 32 positions a chunk of 128 is mostly padding.
+// Up to 32 positions a chunk of 128 is mostly padding, and the recurrence keeps
+// float32's digits in what it multiplies.  Its time grows with the positions:
+// forward of 256 x T x 12 heads of 64, 46 us for 8, 77 for 16 and 137 for 32,
+// where a chunk takes 75 whatever it holds; 64 x T x 16 of 128, 49, 77 and 137
+// against 52; gradients 121, 204 and 431 against 200; one sequence of 12 heads
+// of 64, 12, 18 and 30 against 8.  So over many sequences it is the faster one
+// as well up to about 8 positions (16 of heads up to 64), and from there to 32
+// the digits cost up to two or three times the time (one sequence: almost four).
 bool uses_tc(const Dims &d) { return d.dtype == WKV_BF16 && d.T > 32 && d.D % 8 == 0 && d.M % 8 == 0; }
 
 // Bytes of the segments' states of `n` passes of X x Y launched together.

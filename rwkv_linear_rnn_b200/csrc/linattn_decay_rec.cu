@@ -9,7 +9,7 @@
 // more than the products they replace) and multiplies R by lam^8 once.  Where
 // lam^8 < 2^-16 that would cost range, and R is multiplied at each position.
 // (8 x 1024 x 12 heads of 64, forward: 469 us with three FMAs, one at a time;
-// 188 with two-wide ones; 85 with fetches and strides that cost no arithmetic.)
+// 188 with two-wide ones; 86 with fetches and strides that cost no arithmetic.)
 //
 // The kernel is bound by the FMA pipes: it serves float32 tensors (which the
 // tensor cores' bfloat16 products would round), heads and strides that TMA
@@ -504,8 +504,8 @@ int64_t rec_segments(int64_t BH, int64_t T, int X, int Y, int npass, int sms) {
   // scheduler's, and at least 330 from one to the next; 12 warps fit an SM at
   // a time.  A head in several segments costs its sums (half of that again),
   // the scan and a launch more.  (8 x 1024 x 12 heads of 64: forward 174 us in
-  // one segment, 85 in the 6 that this gives; backward 175 us in the one that it
-  // gives, 224 in 2.)
+  // one segment, 86 in the 6 that this gives, 87 with states in and out;
+  // backward 175 us in the one that it gives, 224 in 2.)
   const int64_t warps = npass * BH * ((Y + 31) / 32) * (X <= 64 ? 1 : 2);
   const double each = X <= 32 ? 160. : 290., chain = X <= 32 ? 220. : 330.;
   int64_t best = 1;
