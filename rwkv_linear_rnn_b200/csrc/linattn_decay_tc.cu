@@ -334,8 +334,8 @@ struct Chunks {
 // State warpgroup: R at the chunk's start -> its bfloat16 copy in shared memory
 // and, decayed, tensor memory again.  A thread is a row of the state.
 template <int XP, int YP, bool OUT, bool TWO>
-__device__ __forceinline__ void state_role(const Pass &p, const Waits &lim, Bars *s, uint8_t *sm, const Chunks &ch, int64_t unit, float g,
-                                           float *result) {
+__device__ __forceinline__ void state_role(const Pass &p, const Waits &lim, Bars *s, uint8_t *sm, const Chunks &ch,
+                                           int64_t unit, float g, float *result) {
   using Ti = Tiles<XP, YP, OUT, TWO>;
   const int x = threadIdx.x, warp = x >> 5;
   const int64_t bh = unit / p.nseg;
@@ -426,7 +426,8 @@ __device__ __forceinline__ void state_role(const Pass &p, const Waits &lim, Bars
 // Key warpgroup: lam^n b as two bfloat16 terms, the second in b's place once
 // its scores are formed; a thread has a row (position).
 template <int XP, int YP, bool OUT, bool TWO>
-__device__ __forceinline__ void keys_role(const Pass &p, const Waits &lim, Bars *s, uint8_t *sm, const Chunks &ch, float g2, bool more) {
+__device__ __forceinline__ void keys_role(const Pass &p, const Waits &lim, Bars *s, uint8_t *sm, const Chunks &ch, float g2,
+                                          bool more) {
   using Ti = Tiles<XP, YP, OUT, TWO>;
   const int j = threadIdx.x - 32 * Roles<OUT, TWO>::KEYS;
   Place<Ti::NS> place;
@@ -618,8 +619,8 @@ struct Outputs {
 // Loads: the tiles of each chunk in the ring's order, each as soon as its slot
 // is free; one whole warp.
 template <int XP, int YP, bool OUT, bool TWO>
-__device__ __forceinline__ void load_role(const Pass &p, const Waits &lim, Bars *s, uint32_t sm, const Chunks &ch, int b, int h,
-                                          const CUtensorMap *am, const CUtensorMap *bm, const CUtensorMap *cm) {
+__device__ __forceinline__ void load_role(const Pass &p, const Waits &lim, Bars *s, uint32_t sm, const Chunks &ch, int b,
+                                          int h, const CUtensorMap *am, const CUtensorMap *bm, const CUtensorMap *cm) {
   using Ti = Tiles<XP, YP, OUT, TWO>;
   Place<Ti::NS> place;
   int n = 0;  // tiles whose loads were issued
@@ -645,13 +646,15 @@ __device__ __forceinline__ void load_role(const Pass &p, const Waits &lim, Bars 
   }
   // The loads in flight write shared memory that outlives this warp, not the
   // CTA: every one is waited for (in order to end; consumers wait for theirs).
-  for (int k = max(0, n - Ti::NS); k < n; ++k) ok = spin(smem_addr(&s->full[k % Ti::NS]), (k / Ti::NS) & 1, kTries) && ok;
+  for (int k = max(0, n - Ti::NS); k < n; ++k)
+    ok = spin(smem_addr(&s->full[k % Ti::NS]), (k / Ti::NS) & 1, kTries) && ok;
   if (!ok) gave_up(lim);
 }
 
 // MMAs, in the order that the head of this file explains; one whole warp.
 template <int XP, int YP, bool OUT, bool TWO>
-__device__ __forceinline__ void mma_role(const Pass &p, const Waits &lim, Bars *s, uint32_t sm, const Chunks &ch, bool more) {
+__device__ __forceinline__ void mma_role(const Pass &p, const Waits &lim, Bars *s, uint32_t sm, const Chunks &ch,
+                                         bool more) {
   using Ti = Tiles<XP, YP, OUT, TWO>;
   using Co = Cols<YP, TWO>;
   constexpr uint32_t SCORES = Co::SCORES, O1 = Co::O1, O2 = Co::O2, ST = Co::ST;
@@ -756,7 +759,9 @@ __device__ __forceinline__ void mma_role(const Pass &p, const Waits &lim, Bars *
   if (elect_one()) {
     mma_commit(smem_addr(&s->drain));
     bool ended = spin(smem_addr(&s->drain), 0, kTries);
-    auto last_of = [&](uint64_t &bar, int n) { ended = (n == 0 || spin(smem_addr(&bar), (n - 1) & 1, kTries)) && ended; };
+    auto last_of = [&](uint64_t &bar, int n) {
+      ended = (n == 0 || spin(smem_addr(&bar), (n - 1) & 1, kTries)) && ended;
+    };
     last_of(s->scores, done.scores);
     last_of(s->w_free, done.keys);
     last_of(s->state, done.states);
